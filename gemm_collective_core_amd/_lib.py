@@ -1,4 +1,5 @@
-"""Loads ``libmc2.so`` and declares the C ABI of ``include/mc2.h``."""
+"""Loads ``libmc2.so`` and declares the C ABI of ``include/mc2.h`` and
+``include/mc2_train.h``."""
 from __future__ import annotations
 
 import ctypes as C
@@ -41,6 +42,16 @@ SIGNATURES = {
     "mc2_version": (C.c_char_p, []),
 }
 
+# Entry points of include/mc2_train.h
+TRAIN_SIGNATURES = {
+    "mc2_moe_unpermute_backward": (_I, [_P, _P, _I64, _P, _P, _P, _I64, _I, _I64, _I, _P, _P, _P,
+                                        _P]),
+    "mc2_moe_permute_backward": (_I, [_P, _I64, _P, _I64, _I, _I64, _I, _P, _P, _P]),
+    "mc2_ns_workspace_size": (C.c_size_t, [_I64, _I64, _I64]),
+    "mc2_ns_orthogonalize": (_I, [_P, _I64, _I64, _I64, _I, _I, _P, C.c_float, C.c_float, _I, _P,
+                                  _P, C.c_size_t, _P]),
+}
+
 _lib = None
 
 
@@ -52,7 +63,7 @@ def load() -> C.CDLL:
             raise RuntimeError(
                 f"{LIB_PATH} is missing: build it with `python -m gemm_collective_core_amd.build`")
         lib = C.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **TRAIN_SIGNATURES}.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args

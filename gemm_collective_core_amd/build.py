@@ -14,7 +14,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmc2.so")
-SOURCES = ["mc2_gemm.hip", "mc2_allreduce.hip", "mc2_grouped.hip", "mc2_moe.hip"]
+SOURCES = ["mc2_gemm.hip", "mc2_allreduce.hip", "mc2_grouped.hip", "mc2_moe.hip",
+           "mc2_moe_bwd.hip", "mc2_ns.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

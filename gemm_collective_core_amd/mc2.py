@@ -1,4 +1,4 @@
-"""Thin Python binding over the C ABI of ``include/mc2.h``.
+"""Thin Python binding over the C ABI of ``include/mc2.h`` and ``include/mc2_train.h``.
 
 Every function has the name of the C entry point it calls and only marshals
 arguments: it checks that tensors live on the GPU with the expected dtype and
@@ -7,6 +7,8 @@ layout, passes their data pointers and the current HIP stream, and raises
 library; there is no other code path.
 """
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
@@ -513,4 +515,102 @@ def mc2_moe_unpermute(y_full, unpermute_idx, probs, *, out=None, dev_err=None):
         y_full.data_ptr(), y_full.shape[0], unpermute_idx.data_ptr(), probs.data_ptr(), T, K, H,
         out.data_ptr(), _ptr(dev_err), _stream(dev))
     _check("mc2_moe_unpermute", st)
+    return out
+
+
+def mc2_moe_unpermute_backward(dout, y_full, unpermute_idx, sorted_idx, probs, *, dy=None,
+                               dprobs=None, need_dy=True, need_dprobs=True, dev_err=None):
+    """Gradient of mc2_moe_unpermute: returns (dy, dprobs), None in the place
+    of one that is not needed. dy (rows of y_full, H) gets the rows that the
+    slots name; its other rows are left as they were (undefined where dy is
+    allocated here). sorted_idx and unpermute_idx are mc2_moe_permute's.
+    dprobs (T, K) fp32."""
+    if probs.dim() != 2 or dout.dim() != 2 or y_full.dim() != 2:
+        raise ValueError("probs must be (T, K), dout (T, H) and y_full (rows, H)")
+    if not (need_dy or need_dprobs):
+        raise ValueError("nothing to compute: need_dy and need_dprobs are both false")
+    T, K = probs.shape
+    H = dout.shape[1]
+    _want(dout, "dout", shape=(T, H), dtypes=_FLOAT16)
+    _want(y_full, "y_full", shape=(y_full.shape[0], H), dtype=dout.dtype)
+    _want(probs, "probs", dtype=torch.float32)
+    _want(unpermute_idx, "unpermute_idx", dtype=torch.int32, numel=T * K)
+    _want(sorted_idx, "sorted_idx", dtype=torch.int32, numel=T * K)
+    _want(dy, "dy", shape=y_full.shape, dtype=dout.dtype)
+    _want(dprobs, "dprobs", shape=(T, K), dtype=torch.float32)
+    _want(dev_err, "dev_err", **_ERR)
+    dev = _dev(dout, y_full, unpermute_idx, sorted_idx, probs, dy, dprobs, dev_err)
+    dy = (torch.empty_like(y_full) if dy is None else dy) if need_dy else None
+    if need_dprobs and dprobs is None:
+        dprobs = torch.empty((T, K), dtype=torch.float32, device=dev)
+    dprobs = dprobs if need_dprobs else None
+    with torch.cuda.device(dev):
+        st = _lib.load().mc2_moe_unpermute_backward(
+            dout.data_ptr(), y_full.data_ptr(), y_full.shape[0], unpermute_idx.data_ptr(),
+            sorted_idx.data_ptr(), probs.data_ptr(), T, K, H, _CODES[dout.dtype], _ptr(dy),
+            _ptr(dprobs), _ptr(dev_err), _stream(dev))
+    _check("mc2_moe_unpermute_backward", st)
+    return dy, dprobs
+
+
+def mc2_moe_permute_backward(dpermuted, unpermute_idx, topk, *, dx=None, dev_err=None):
+    """Gradient of mc2_moe_permute's row grouping: dx (T, H), the sum of each
+    token's topk rows of dpermuted; unpermute_idx (T * topk) int32."""
+    if dpermuted.dim() != 2:
+        raise ValueError("dpermuted must be (rows, H)")
+    if topk < 1 or unpermute_idx.numel() % topk:
+        raise ValueError("unpermute_idx must hold T * topk elements")
+    T, H = unpermute_idx.numel() // topk, dpermuted.shape[1]
+    _want(dpermuted, "dpermuted", dtypes=_FLOAT16)
+    _want(unpermute_idx, "unpermute_idx", dtype=torch.int32)
+    _want(dx, "dx", shape=(T, H), dtype=dpermuted.dtype)
+    _want(dev_err, "dev_err", **_ERR)
+    dev = _dev(dpermuted, unpermute_idx, dx, dev_err)
+    if dx is None:
+        dx = torch.empty((T, H), dtype=dpermuted.dtype, device=dev)
+    with torch.cuda.device(dev):
+        st = _lib.load().mc2_moe_permute_backward(
+            dpermuted.data_ptr(), dpermuted.shape[0], unpermute_idx.data_ptr(), T, topk, H,
+            _CODES[dpermuted.dtype], dx.data_ptr(), _ptr(dev_err), _stream(dev))
+    _check("mc2_moe_permute_backward", st)
+    return dx
+
+
+MC2_NS_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def mc2_ns_workspace_size(batch, m, n) -> int:
+    return int(_lib.load().mc2_ns_workspace_size(batch, m, n))
+
+
+def mc2_ns_orthogonalize(g, *, steps=5, coeffs=MC2_NS_COEFFS, eps=1e-7, scale=1.0,
+                         out_dtype=torch.bfloat16, out=None, workspace=None):
+    """scale times the Newton-Schulz orthogonalisation of each matrix of g,
+    (m, n) or a stack (batch, m, n) of fp32, bf16 or fp16; out has g's shape and
+    out_dtype (bf16 or fp16). coeffs: one (a, b, c) for every step, or `steps` of
+    them."""
+    if g.dim() not in (2, 3):
+        raise ValueError("g must be (m, n) or a stack (batch, m, n)")
+    _want(g, "g", dtypes=(torch.float32, *_FLOAT16))
+    out_dtype = out_dtype if out is None else out.dtype
+    if out_dtype not in _FLOAT16:
+        raise ValueError(f"out_dtype must be one of {_FLOAT16}, got {out_dtype}")
+    _want(out, "out", shape=g.shape)
+    _want(workspace, "workspace", dtype=torch.uint8)
+    flat = [float(v) for t in coeffs for v in (t if isinstance(t, (tuple, list)) else (t,))]
+    if len(flat) == 3:
+        flat = flat * max(steps, 0)
+    if len(flat) != 3 * steps:
+        raise ValueError("coeffs must be one (a, b, c), or one for each step")
+    dev = _dev(g, out, workspace)
+    batch, (m, n) = (1 if g.dim() == 2 else g.shape[0]), g.shape[-2:]
+    if out is None:
+        out = torch.empty(g.shape, dtype=out_dtype, device=dev)
+    workspace = _workspace(mc2_ns_workspace_size(batch, m, n), workspace, dev)
+    with torch.cuda.device(dev):
+        st = _lib.load().mc2_ns_orthogonalize(
+            g.data_ptr(), batch, m, n, _CODES[g.dtype], steps,
+            (ctypes.c_float * len(flat))(*flat), eps, scale, _CODES[out_dtype], out.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _stream(dev))
+    _check("mc2_ns_orthogonalize", st)
     return out

@@ -447,4 +447,7 @@ const char* mc2_version(void);
 }
 #endif
 
+/* The training-step operators around the grouped experts, from the same library. */
+#include "mc2_train.h"
+
 #endif /* MC2_H_ */
