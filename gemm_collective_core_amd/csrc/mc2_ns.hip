@@ -23,7 +23,7 @@
 // then 1e-3 whatever the rank. The last step reads hi only, since what it
 // loses is not multiplied again.
 #include "../../include/mc2_train.h"
-#include "mc2_common.hpp"
+#include "gemm_core.hpp"
 #include "mc2_host.hpp"
 
 namespace mc2 {
@@ -184,37 +184,48 @@ struct NsArgs {
   int out_bf16;
 };
 
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-
-// Swizzled place of 16-byte chunk ch (8 columns) of k row kr in a k-major
-// stage W columns wide: 32-byte pairs move so that the 16 k rows that one
-// transposing read touches fall on different banks.
-template <int W>
-__device__ __forceinline__ int ns_kpos(int kr, int ch) {
-  const int swz = W == 128 ? (kr & 3) | (((kr >> 3) & 1) << 2) : ((kr >> 1) & 1) | (((kr >> 3) & 1) << 1);
-  return kr * (W * 2) + (((ch >> 1) ^ swz) << 5) + ((ch & 1) << 4);
+// Tile of workgroup b of n: workgroups go to the 8 XCDs in turn, so XCD x takes
+// the x-th eighth of the tiles, whose rows and columns its L2 then shares (with
+// 8 or 16 matrices, whole matrices).
+__device__ __forceinline__ int ns_xcd_tile(int b, int n) {
+  const int x = b & 7, q = n >> 3, rest = n & 7;
+  return x * q + (x < rest ? x : rest) + (b >> 3);
 }
-// Place of 16-byte chunk c of row r in a K-contiguous stage (128-byte rows).
-__device__ __forceinline__ int ns_rpos(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
 
-// One W x W tile of a product. 4 waves as 2 x 2, K in stages of 64 through a
-// two-buffer LDS ring: the next stage is loaded into registers while this one
-// is multiplied. Each MFMA takes the second operand's fragment first, so a
-// lane ends with four consecutive columns of one row.
+// Swizzle of the 32-byte pairs (16 columns) of k row kr in a k-major stage W
+// columns wide: the 16 k rows that one transposing read touches then fall on
+// different banks. It depends on bits 0, 1 and 3 of kr only.
+template <int W>
+__device__ __forceinline__ int ns_kswz(int kr) {
+  return W == 128 ? (kr & 3) | (((kr >> 3) & 1) << 2) : ((kr >> 1) & 1) | (((kr >> 3) & 1) << 1);
+}
+
+// One W x W tile of a product. 4 waves as 2 x 2; K in stages of 64 through a
+// ring of NS LDS buffers, filled by loads straight to LDS that run NS - 1
+// stages ahead; two workgroups share a CU, so one multiplies while the other
+// waits at its barrier. W = 128 takes 64 KiB of LDS with NS = 2, W = 64 with
+// NS = 4 (its stages are four times shorter, and the loads' latency is not).
+// Each MFMA takes the second operand's fragment first, so a lane ends with
+// four consecutive columns of one row.
 template <int W, int MODE>
-__global__ __launch_bounds__(kNsThreads) void ns_gemm_kernel(NsArgs p) {
+__global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
   constexpr bool KMAJ = MODE == kGram;
   constexpr bool SYM = MODE == kGram || MODE == kSquare;
   constexpr int OB = W * 128;      // bytes of one operand's stage
-  constexpr int NL = W / 32;       // 16-byte loads per thread, operand and stage
+  constexpr int NS = W == 128 ? 2 : 4;
+  constexpr int NL = OB / 4096;    // 1 KiB loads per wave, operand and stage
   constexpr int F = W / 32;        // 16-row fragments per wave and operand
+  constexpr int NR = KMAJ ? 4 * F : 2 * F;  // LDS reads per wave and k-step
   constexpr int PITCH = W * 2 + 16;
-  __shared__ __attribute__((aligned(16))) char smem[4 * OB];
-  static_assert(W * PITCH <= 4 * OB, "the output tile is staged in the operands' place");
+  __shared__ __attribute__((aligned(16))) char smem_raw[NS * 2 * OB];
+  static_assert(W * PITCH <= NS * 2 * OB, "the output tile is staged in the operands' place");
+  lds_t* smem = (lds_t*)smem_raw;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int b = blockIdx.x / p.tiles;
-  int t = blockIdx.x - b * p.tiles;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lt = ns_xcd_tile(blockIdx.x, gridDim.x);
+  const int b = lt / p.tiles;
+  int t = lt - b * p.tiles;
   int tm, tn;
   if constexpr (SYM) {
     tm = 0;
@@ -239,30 +250,45 @@ __global__ __launch_bounds__(kNsThreads) void ns_gemm_kernel(NsArgs p) {
   const int nbn = MODE == kOutWide ? p.cp : p.rp;
   const int stages = (KMAJ ? p.cp : p.rp) / 64;
 
-  // this thread's loads: source of stage 0, LDS place
-  const u32x4_t* src[2][NL];
-  int dst[NL];
+  // Byte offsets of this wave's loads: a load fills 1 KiB of LDS linearly, so
+  // the lane's place there says which piece of the operand it takes. Rows or
+  // columns beyond the matrix read its last ones; they are not stored.
+  uint32_t off[2][NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
-    const int q = tid + i * kNsThreads;
+    const int o = (wave * NL + i) * 1024 + lane * 16;
     if constexpr (KMAJ) {
-      const int kr = q / (W / 8), ch = q - kr * (W / 8);
-      // columns beyond the matrix read its last ones; they are not stored
-      const int ca = row0 + ch * 8 < na ? row0 + ch * 8 : na - 8;
-      const int cb = col0 + ch * 8 < nbn ? col0 + ch * 8 : nbn - 8;
-      src[0][i] = reinterpret_cast<const u32x4_t*>(opa + (int64_t)kr * p.rp + ca);
-      src[1][i] = reinterpret_cast<const u32x4_t*>(opb + (int64_t)kr * p.rp + cb);
-      dst[i] = ns_kpos<W>(kr, ch);
+      const int kr = o / (W * 2), in = o - kr * (W * 2);
+      const int col = (((in >> 5) ^ ns_kswz<W>(kr)) << 4) + ((in & 16) >> 1);
+      const int ca = row0 + col < na ? row0 + col : na - 8;
+      const int cb = col0 + col < nbn ? col0 + col : nbn - 8;
+      off[0][i] = static_cast<uint32_t>((kr * p.rp + ca) * 2);
+      off[1][i] = static_cast<uint32_t>((kr * p.rp + cb) * 2);
     } else {
-      const int r = q >> 3, ch = q & 7;
-      const int ra = row0 + r < na ? row0 + r : na - 1;
-      const int rb = col0 + r < nbn ? col0 + r : nbn - 1;
-      src[0][i] = reinterpret_cast<const u32x4_t*>(opa + (int64_t)ra * p.rp + ch * 8);
-      src[1][i] = reinterpret_cast<const u32x4_t*>(opb + (int64_t)rb * p.rp + ch * 8);
-      dst[i] = ns_rpos(r, ch);
+      const int r = o >> 7, ch = ((o >> 4) & 7) ^ ((r >> 1) & 7);
+      const int ra = row0 + r < na ? r : na - 1 - row0;
+      const int rb = col0 + r < nbn ? r : nbn - 1 - col0;
+      off[0][i] = static_cast<uint32_t>(ra * p.rp * 2 + ch * 16);
+      off[1][i] = static_cast<uint32_t>(rb * p.rp * 2 + ch * 16);
     }
   }
-  const int64_t step = KMAJ ? (int64_t)8 * p.rp : 8;  // 16-byte pieces per stage
+  const char* base_a = reinterpret_cast<const char*>(KMAJ ? opa : opa + (int64_t)row0 * p.rp);
+  const char* base_b = reinterpret_cast<const char*>(KMAJ ? opb : opb + (int64_t)col0 * p.rp);
+  const int64_t step = KMAJ ? (int64_t)128 * p.rp : 128;  // bytes per stage
+  auto issue = [&](int s) {
+    // a stage past the last one gets resources of no records: its loads touch
+    // no memory, and the count of loads in flight stays the same
+    const int nrec = s < stages ? 0x7ffffff0 : 0;
+    const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base_a + s * step), 0, nrec,
+                                                      kBufFlags);
+    const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base_b + s * step), 0, nrec,
+                                                      kBufFlags);
+    lds_t* d = smem + (s % NS) * 2 * OB + wave * NL * 1024;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) dma16(ra, d + i * 1024, off[0][i]);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) dma16(rb, d + OB + i * 1024, off[1][i]);
+  };
 
   f32x4_t acc[F][F];
 #pragma unroll
@@ -271,64 +297,85 @@ __global__ __launch_bounds__(kNsThreads) void ns_gemm_kernel(NsArgs p) {
     for (int j = 0; j < F; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int wr = (wave >> 1) * (W / 2), wc = (wave & 1) * (W / 2);
 
-  auto frag = [&](const char* s, int x0, int ks) {
-    if constexpr (KMAJ) {
-      const int j = lane & 15, g = lane >> 4;
-      const int kr = ks * 32 + g * 8 + (j >> 2);
-      // the half h = 1 lies 4 k rows on, where the swizzle is the same for
-      // W = 128 and for W = 64 (bits 0, 1 and 3 of the k row)
-      const char* q = s + ns_kpos<W>(kr, x0 >> 3) + ((j & 3) << 3);
-      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) s16x4_t*)(q));
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) s16x4_t*)(q + 4 * W * 2));
-      const u32x2_t l2 = bit_cast<u32x2_t>(lo), h2 = bit_cast<u32x2_t>(hi);
-      return bit_cast<f16x8_t>(u32x4_t{l2[0], l2[1], h2[0], h2[1]});
-    } else {
-      return *reinterpret_cast<const f16x8_t*>(s + ns_rpos(x0 + (lane & 15), ks * 4 + (lane >> 4)));
-    }
+  // Operand fragments of one k-step: a lane supplies row lane & 15 of each 16
+  // rows, K values 8 (lane >> 4) .. + 7 of the step's 32; from a k-major stage
+  // as two transposing 8-byte reads of 4 k rows each.
+  struct Frags {
+    u32x4_t q[KMAJ ? 1 : F];
+    u32x2_t h[KMAJ ? F : 1][2];
   };
-
-  u32x4_t va[NL], vb[NL];
+  const uint32_t s0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
+  auto read = [&](Frags& f, uint32_t s, int x0, int ks) {
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    va[i] = src[0][i][0];
-    vb[i] = src[1][i][0];
-  }
-  for (int s = 0; s < stages; ++s) {
-    char* sa = smem + (s & 1) * 2 * OB;
-    char* sb = sa + OB;
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      *reinterpret_cast<u32x4_t*>(sa + dst[i]) = va[i];
-      *reinterpret_cast<u32x4_t*>(sb + dst[i]) = vb[i];
-    }
-    __syncthreads();
-    if (s + 1 < stages) {
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        va[i] = src[0][i][(s + 1) * step];
-        vb[i] = src[1][i][(s + 1) * step];
+    for (int i = 0; i < F; ++i) {
+      if constexpr (KMAJ) {
+        const int j = lane & 15, g = lane >> 4;
+        const int kr = ks * 32 + g * 8 + (j >> 2);
+        const uint32_t at = s + kr * (W * 2) + ((((x0 >> 4) + i) ^ ns_kswz<W>(kr)) << 5) + ((j & 3) << 3);
+        asm volatile("ds_read_b64_tr_b16 %0, %1" : "=v"(f.h[i][0]) : "v"(at) : "memory");
+        asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2"
+                     : "=v"(f.h[i][1]) : "v"(at), "i"(4 * W * 2) : "memory");
+      } else {
+        const uint32_t at = s + row_off(x0 + i * 16 + (lane & 15), ks * 4 + (lane >> 4));
+        asm volatile("ds_read_b128 %0, %1" : "=v"(f.q[i]) : "v"(at) : "memory");
       }
     }
+  };
+  // ties the fragments to the wait before it: no use of them moves above
+  auto tie = [&](Frags& f) {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      f16x8_t fa[F], fb[F];
-#pragma unroll
-      for (int i = 0; i < F; ++i) fa[i] = frag(sa, wr + i * 16, ks);
-#pragma unroll
-      for (int i = 0; i < F; ++i) fb[i] = frag(sb, wc + i * 16, ks);
-#pragma unroll
-      for (int i = 0; i < F; ++i)
-#pragma unroll
-        for (int j = 0; j < F; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < F; ++i) {
+      if constexpr (KMAJ) {
+        asm volatile("" : "+v"(f.h[i][0]));
+        asm volatile("" : "+v"(f.h[i][1]));
+      } else {
+        asm volatile("" : "+v"(f.q[i]));
+      }
     }
+  };
+  auto get = [&](const Frags& f, int i) {
+    if constexpr (KMAJ)
+      return bit_cast<f16x8_t>(u32x4_t{f.h[i][0][0], f.h[i][0][1], f.h[i][1][0], f.h[i][1][1]});
+    else
+      return bit_cast<f16x8_t>(f.q[i]);
+  };
+  auto multiply = [&](const Frags& fa, const Frags& fb) {
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(get(fb, j), get(fa, i), acc[i][j], 0, 0, 0);
+  };
+
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s) issue(s);
+  for (int s = 0; s < stages; ++s) {
+    // this wave's loads of stage s have landed (those of the stages after it
+    // may be in flight: loads complete in order), then every wave's; and every
+    // wave is done with the buffer that the next loads fill
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * 2 * NL) : "memory");
+    bar_sync();
+    const uint32_t sa = s0 + (s % NS) * 2 * OB, sb = sa + OB;
+    Frags a0, b0, a1, b1;
+    read(b0, sb, wc, 0);
+    read(a0, sa, wr, 0);
+    issue(s + NS - 1);
+    read(b1, sb, wc, 1);
+    read(a1, sa, wr, 1);
+    lgkm_wait(NR);
+    tie(b0);
+    tie(a0);
+    multiply(a0, b0);
+    lgkm_wait(0);
+    tie(b1);
+    tie(a1);
+    multiply(a1, b1);
   }
+  wait_vmcnt0();
   __syncthreads();  // every read of the operands is done: their place takes the output
 
   auto stage4 = [&](int i, int j, uint32_t x, uint32_t y) {
-    *reinterpret_cast<u32x2_t*>(smem + (wr + i * 16 + (lane & 15)) * PITCH +
+    *reinterpret_cast<MC2_LDS u32x2_t*>(smem + (wr + i * 16 + (lane & 15)) * PITCH +
                                 (wc + j * 16 + 4 * (lane >> 4)) * 2) = u32x2_t{x, y};
   };
   auto pack = [](float x, float y) {
@@ -341,7 +388,7 @@ __global__ __launch_bounds__(kNsThreads) void ns_gemm_kernel(NsArgs p) {
       const int r = q / (W / 8), c8 = (q - r * (W / 8)) * 8;
       if (row0 + r < rows && col0 + c8 < cols)
         *reinterpret_cast<u32x4_t*>(out + (int64_t)(row0 + r) * ld + col0 + c8) =
-            *reinterpret_cast<const u32x4_t*>(smem + r * PITCH + c8 * 2);
+            *reinterpret_cast<const MC2_LDS u32x4_t*>(smem + r * PITCH + c8 * 2);
     }
   };
 
@@ -378,9 +425,9 @@ __global__ __launch_bounds__(kNsThreads) void ns_gemm_kernel(NsArgs p) {
           u32x4_t o;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint16_t x = *reinterpret_cast<const uint16_t*>(smem + (r8 + 2 * e) * PITCH + c * 2);
+            const uint16_t x = *reinterpret_cast<const MC2_LDS uint16_t*>(smem + (r8 + 2 * e) * PITCH + c * 2);
             const uint16_t y =
-                *reinterpret_cast<const uint16_t*>(smem + (r8 + 2 * e + 1) * PITCH + c * 2);
+                *reinterpret_cast<const MC2_LDS uint16_t*>(smem + (r8 + 2 * e + 1) * PITCH + c * 2);
             o[e] = x | (static_cast<uint32_t>(y) << 16);
           }
           *reinterpret_cast<u32x4_t*>(out + (int64_t)(col0 + c) * p.rp + row0 + r8) = o;
@@ -444,10 +491,244 @@ __global__ __launch_bounds__(kNsThreads) void ns_gemm_kernel(NsArgs p) {
         const int r = q / W, c = q - r * W;
         if (row0 + r < p.om && col0 + c < p.on)
           out[(int64_t)(row0 + r) * p.on + col0 + c] =
-              *reinterpret_cast<const uint16_t*>(smem + r * PITCH + c * 2);
+              *reinterpret_cast<const MC2_LDS uint16_t*>(smem + r * PITCH + c * 2);
       }
     }
   }
+}
+
+// ---------------------------------------------------------------- one workgroup per matrix
+
+// A small matrix (rp <= 128 and at most 64 Ki padded elements) is iterated by
+// one workgroup in one launch: launches, not work, are what the general path
+// costs there (17 of them, 60 us for 64 x 256).
+//
+// 8 waves. Y's high half lives in LDS (up to 128 KiB) as rows of rp values;
+// wave w owns 16-row blocks w * RB .. + RB - 1 and holds their values in fp32 in
+// registers, in the accumulator layout: the product Y Q is added onto a Y held
+// there, so no low half is needed, and a wave's update touches its own rows
+// only. A and Q take turns in one (rp, rp) LDS array.
+constexpr int kTinyThreads = 512;
+constexpr int64_t kTinyElems = 65536;
+
+struct TinyArgs {
+  const void* g;
+  uint16_t* out;
+  int m, n, in_dtype, out_bf16, steps;
+  float eps, scale;
+  float co[3 * 32];
+};
+
+// Byte place of 16-byte chunk c of row r: RP values per row. Both the 16 rows
+// that one row-wise fragment read touches and the 16 k rows of a transposing
+// read (rows 8g + 0..3 or 8g + 4..7) spread over the banks.
+template <int RP>
+__device__ __forceinline__ uint32_t tiny_pos(int r, int c) {
+  const int f = RP == 64 ? (r >> 1) & 7 : ((r & 3) << 1) | (((r >> 3) & 1) << 3) | ((r >> 2) & 1);
+  return static_cast<uint32_t>(r * (RP * 2) + ((c ^ f) << 4));
+}
+
+template <int RP>
+__device__ __forceinline__ f16x8_t tiny_row(const char* s, int r0, int ks) {
+  const int lane = threadIdx.x & 63;
+  return *reinterpret_cast<const f16x8_t*>(s + tiny_pos<RP>(r0 + (lane & 15), ks * 4 + (lane >> 4)));
+}
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+// 16 columns at c0 as a fragment over k rows ks * 32 .. + 31
+template <int RP>
+__device__ __forceinline__ f16x8_t tiny_col(const char* s, int c0, int ks) {
+  const int lane = threadIdx.x & 63, j = lane & 15;
+  const int kr = ks * 32 + (lane >> 4) * 8 + (j >> 2);
+  const int c = (c0 >> 3) + ((j & 3) >> 1);
+  s16x4_t h[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (MC2_LDS s16x4_t*)(s + tiny_pos<RP>(kr + 4 * i, c) + ((j & 1) << 3)));
+  const u32x2_t l = bit_cast<u32x2_t>(h[0]), u = bit_cast<u32x2_t>(h[1]);
+  return bit_cast<f16x8_t>(u32x4_t{l[0], l[1], u[0], u[1]});
+}
+
+// four consecutive columns c .. c + 3 of row r
+template <int RP>
+__device__ __forceinline__ void tiny_put(char* s, int r, int c, float a, float b, float x, float y) {
+  const uint32_t lo = f32_to_f16_bits(a) | (static_cast<uint32_t>(f32_to_f16_bits(b)) << 16);
+  const uint32_t hi = f32_to_f16_bits(x) | (static_cast<uint32_t>(f32_to_f16_bits(y)) << 16);
+  *reinterpret_cast<u32x2_t*>(s + tiny_pos<RP>(r, c >> 3) + ((c & 4) << 1)) = u32x2_t{lo, hi};
+}
+
+template <int RP, int RB>
+__global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
+  constexpr int CB = RP / 16, KS = RB * 4;  // 32-row k steps of Y
+  constexpr int FA = RP / 64, FB = RP / 32;  // a wave's 16-row / 16-column blocks of A and Q
+  __shared__ __attribute__((aligned(16))) char s_y[RB * 128 * RP * 2];
+  __shared__ __attribute__((aligned(16))) char s_a[RP * RP * 2];
+  double* s_n = reinterpret_cast<double*>(s_a);  // before A: its first write follows a barrier
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lr = lane & 15, lc = 4 * (lane >> 4);
+  const int m = p.m, n = p.n;
+  const bool tall = m >= n;
+  const int r = tall ? n : m, c = tall ? m : n;
+  const int64_t gb = (int64_t)blockIdx.x * m * n;
+
+  f32x4_t x[RB][CB];
+  double sq = 0;
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) {
+      const int row = (wave * RB + i) * 16 + lr;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = j * 16 + lc + e;
+        float v = 0.f;
+        if (row < c && col < r) {
+          const int64_t at = gb + (tall ? (int64_t)row * n + col : (int64_t)col * n + row);
+          if (p.in_dtype == MC2_F32) v = ns_load<MC2_F32>(p.g, at);
+          else if (p.in_dtype == MC2_BF16) v = ns_load<MC2_BF16>(p.g, at);
+          else v = ns_load<MC2_F16>(p.g, at);
+        }
+        x[i][j][e] = v;
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sq = __builtin_fma((double)x[i][j][e], (double)x[i][j][e], sq);
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) sq += __shfl_xor(sq, off);
+  if (lane == 0) s_n[wave] = sq;
+  __syncthreads();
+  double norm2 = 0;
+#pragma unroll
+  for (int w = 0; w < kTinyThreads / 64; ++w) norm2 += s_n[w];
+  const double inv = norm2 == 0.0 ? 0.0 : kXScale / (sqrt(norm2) + static_cast<double>(p.eps));
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) {
+      const int row = (wave * RB + i) * 16 + lr;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)  // (what lies outside G stays zero: inv may be NaN)
+        if (row < c && j * 16 + lc + e < r)
+          x[i][j][e] = static_cast<float>(static_cast<double>(x[i][j][e]) * inv);
+    }
+
+  const int wm = (wave >> 1) * (RP / 4), wn = (wave & 1) * (RP / 2);  // this wave's part of A, Q
+  for (int s = 0; s < p.steps; ++s) {
+    const float a = p.co[3 * s], b = p.co[3 * s + 1], cc = p.co[3 * s + 2];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+        tiny_put<RP>(s_y, (wave * RB + i) * 16 + lr, j * 16 + lc, x[i][j][0], x[i][j][1],
+                     x[i][j][2], x[i][j][3]);
+    __syncthreads();
+    f32x4_t g[FA][FB];
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) g[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int ks = 0; ks < KS; ++ks) {
+      f16x8_t fa[FA], fb[FB];
+#pragma unroll
+      for (int i = 0; i < FA; ++i) fa[i] = tiny_col<RP>(s_y, wm + i * 16, ks);
+#pragma unroll
+      for (int j = 0; j < FB; ++j) fb[j] = tiny_col<RP>(s_y, wn + j * 16, ks);
+#pragma unroll
+      for (int i = 0; i < FA; ++i)
+#pragma unroll
+        for (int j = 0; j < FB; ++j)
+          g[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], g[i][j], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[i][j][e] *= kGramScale;
+        tiny_put<RP>(s_a, wm + i * 16 + lr, wn + j * 16 + lc, g[i][j][0], g[i][j][1], g[i][j][2],
+                     g[i][j][3]);
+      }
+    __syncthreads();
+    f32x4_t q[FA][FB];
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) q[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < RP / 32; ++ks) {
+      f16x8_t fa[FA], fb[FB];
+#pragma unroll
+      for (int i = 0; i < FA; ++i) fa[i] = tiny_row<RP>(s_a, wm + i * 16, ks);
+#pragma unroll
+      for (int j = 0; j < FB; ++j) fb[j] = tiny_row<RP>(s_a, wn + j * 16, ks);
+#pragma unroll
+      for (int i = 0; i < FA; ++i)
+#pragma unroll
+        for (int j = 0; j < FB; ++j)
+          q[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], q[i][j], 0, 0, 0);
+    }
+    __syncthreads();  // every read of A is done: Q takes its place
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[i][j][e] = b * g[i][j][e] + cc * (q[i][j][e] * kSqScale);
+        tiny_put<RP>(s_a, wm + i * 16 + lr, wn + j * 16 + lc, q[i][j][0], q[i][j][1], q[i][j][2],
+                     q[i][j][3]);
+      }
+    __syncthreads();
+    // x = a x + Y Q: the product's scale is 2^21, x's 2^12
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i][j][e] *= a * (1.f / kUpdScale);
+#pragma unroll
+    for (int ks = 0; ks < RP / 32; ++ks) {
+      f16x8_t fa[RB];
+#pragma unroll
+      for (int i = 0; i < RB; ++i) fa[i] = tiny_row<RP>(s_y, (wave * RB + i) * 16, ks);
+#pragma unroll
+      for (int j = 0; j < CB; ++j) {
+        const f16x8_t fb = tiny_row<RP>(s_a, j * 16, ks);
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+          x[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb, fa[i], x[i][j], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i][j][e] *= kUpdScale;
+    // (a wave reads only its own rows of Y above and writes only them in the
+    // next step; the reads of Q end before that step's first barrier)
+  }
+  const float sc = p.scale / kXScale;
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) {
+      const int row = (wave * RB + i) * 16 + lr;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = j * 16 + lc + e;
+        const float v = x[i][j][e] * sc;
+        if (row < c && col < r)
+          p.out[gb + (tall ? (int64_t)row * n + col : (int64_t)col * n + row)] =
+              p.out_bf16 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v);
+      }
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -524,6 +805,28 @@ static void ns_product(NsArgs p, int64_t batch, hipStream_t stream) {
   }
 }
 
+// The whole call as one launch, for matrices that one workgroup can hold.
+// Returns false for others.
+static bool ns_tiny(const TinyArgs& p, int64_t batch, const NsLayout& L, hipStream_t stream) {
+  const int64_t rb = (L.cp + 127) / 128;
+  int64_t pow2 = 1;
+  while (pow2 < rb) pow2 *= 2;
+  if (L.rp > 128 || pow2 * 128 * L.rp > kTinyElems) return false;
+  const dim3 grid(static_cast<unsigned>(batch)), blk(kTinyThreads);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, blk, 0, stream, p); };
+  if (L.rp == 64) {
+    if (pow2 == 1) go(ns_tiny_kernel<64, 1>);
+    else if (pow2 == 2) go(ns_tiny_kernel<64, 2>);
+    else if (pow2 == 4) go(ns_tiny_kernel<64, 4>);
+    else go(ns_tiny_kernel<64, 8>);
+  } else {
+    if (pow2 == 1) go(ns_tiny_kernel<128, 1>);
+    else if (pow2 == 2) go(ns_tiny_kernel<128, 2>);
+    else go(ns_tiny_kernel<128, 4>);
+  }
+  return true;
+}
+
 }  // namespace mc2
 
 using namespace mc2;
@@ -549,6 +852,18 @@ extern "C" int mc2_ns_orthogonalize(const void* g, int64_t batch, int64_t m, int
   // grids are 32-bit: tiles of 64 x 64 of the largest product
   if (batch * (L.cp / 64) * (L.cp / 64) > 0x7fffffff) return MC2_ERR_SHAPE;
   if (ws_bytes < L.total) return MC2_ERR_WORKSPACE;
+  TinyArgs ta{};
+  ta.g = g;
+  ta.out = static_cast<uint16_t*>(out);
+  ta.m = static_cast<int>(m);
+  ta.n = static_cast<int>(n);
+  ta.in_dtype = in_dtype;
+  ta.out_bf16 = out_dtype == MC2_BF16;
+  ta.steps = steps;
+  ta.eps = eps;
+  ta.scale = scale;
+  for (int i = 0; i < 3 * steps; ++i) ta.co[i] = coeffs[i];
+  if (ns_tiny(ta, batch, L, stream)) return hipGetLastError() == hipSuccess ? MC2_OK : MC2_ERR_HIP;
   char* ws = static_cast<char*>(workspace);
   double* part = reinterpret_cast<double*>(ws + L.part);
   uint16_t* y[2] = {reinterpret_cast<uint16_t*>(ws + L.y0), reinterpret_cast<uint16_t*>(ws + L.y1)};
