@@ -6,22 +6,23 @@
 // tall, Y = X^T for a wide G: (cp, rp), rows of rp values, both padded with
 // zeros to multiples of 64. Then
 //   A  = Y^T Y                 contraction over the rows of Y (k-major reads)
-//   Q  = b A + c A A           A is symmetric: both operands are its rows
-//   Y' = a Y + Y Q             Q is symmetric: Y's rows by Q's rows
+//   Q~ = a I + b A + c A A     A is symmetric: both operands are its rows
+//   Y' = Y Q~                  Q~ is symmetric: Y's rows by its rows
 // and the last step writes out = scale * Y Q~ (G tall) or scale * Q~ Y^T (G
-// wide: the same two operands the other way round), Q~ = a I + Q.
+// wide: the same two operands the other way round).
 //
 // Number formats. The products run on the fp16 matrix instructions with fp32
 // accumulation: fp16 and bf16 run at the same rate and fp16 has three bits
 // more (errors of the result 1e-3 instead of 1e-2). Powers of two keep the
-// values in its range: Y is stored times 2^12 (entries up to 16), A and Q
+// values in its range: Y is stored times 2^12 (entries up to 16), A and Q~
 // times 2^9 (entries up to 128). Rounding Y to fp16 alone would not do: noise
 // in a direction whose singular value is near zero (a gradient of fewer rows
 // than the matrix has) grows by the factor a in every step, 484 times in five
-// steps, and reached 1.5e-1 of the result. So Y is held as hi + lo, two fp16
-// (lo 2^11 times finer): the products use hi, the term a Y both. Errors are
-// then 1e-3 whatever the rank. The last step reads hi only, since what it
-// loses is not multiplied again.
+// steps, and reached 1.5e-1 of the result. So Y is held as hi + lo, two fp16 (lo
+// times 2^11 more): the products use hi,
+//   Y' = hi Q~ + a lo,  Q~ = a I + b A + c A A,
+// and errors are 1e-3 to 2.5e-3 whatever the rank. The last step leaves lo
+// out, since what it loses is not multiplied again.
 #include "../../include/mc2_train.h"
 #include "gemm_core.hpp"
 #include "mc2_host.hpp"
@@ -108,9 +109,22 @@ __global__ __launch_bounds__(kNsThreads) void ns_norm_kernel(const void* __restr
 }
 
 // x (in Y's scale) -> its two fp16 halves
-__device__ __forceinline__ void ns_split(float x, uint16_t& hi, uint16_t& lo) {
+__device__ __forceinline__ void ns_split(float x, uint32_t& hi, uint32_t& lo) {
   hi = f32_to_f16_bits(x);
   lo = f32_to_f16_bits((x - f16_bits_to_f32(hi)) * kLoScale);
+}
+
+// lo is kept in the order in which the update's lanes hold it, so that it moves
+// in whole 512-byte pieces straight between registers and memory: by W x W tile,
+// wave (2 x 2), 16 x 16 block, lane, each lane's 8 bytes holding four consecutive
+// columns of one row. Index of the 8 bytes of (row, col), col a multiple of 4.
+__device__ __forceinline__ int64_t ns_lo_place(int row, int col, int w, int tiles_n) {
+  const int h = w / 2, f = w / 32;
+  const int tile = (row / w) * tiles_n + col / w;
+  const int in_r = row % w, in_c = col % w;
+  const int wave = (in_r / h) * 2 + in_c / h;
+  const int blk = (in_r % h) / 16 * f + (in_c % h) / 16;
+  return ((int64_t)(tile * 4 + wave) * (f * f) + blk) * 64 + (row & 15) + ((col >> 2) & 3) * 16;
 }
 
 // One 64 x 64 tile of Y = G / (|G| + eps), transposed for a wide G, with zeros
@@ -118,7 +132,8 @@ __device__ __forceinline__ void ns_split(float x, uint16_t& hi, uint16_t& lo) {
 template <int D, bool TALL, bool VEC>
 __global__ __launch_bounds__(kNsThreads) void ns_init_kernel(
     const void* __restrict__ g, int64_t m, int64_t n, const double* __restrict__ part, int nb,
-    float eps, int64_t cp, int64_t rp, uint16_t* __restrict__ yhi, uint16_t* __restrict__ ylo) {
+    float eps, int64_t cp, int64_t rp, uint16_t* __restrict__ yhi, u32x2_t* __restrict__ ylo,
+    int64_t lo_size, int w, int tiles_n) {
   __shared__ float s_t[64][65];
   const int b = blockIdx.y, tid = threadIdx.x;
   const double norm2 = block_sum(tid < nb ? part[(int64_t)b * nb + tid] : 0.0);
@@ -147,20 +162,25 @@ __global__ __launch_bounds__(kNsThreads) void ns_init_kernel(
     }
   }
   __syncthreads();
+  auto at = [&](int r, int c) { return TALL ? s_t[r][c] : s_t[c][r]; };
   for (int i = tid; i < 64 * 8; i += kNsThreads) {
     const int r = i >> 3, c8 = (i & 7) * 8;
-    u32x4_t h, l;
+    u32x4_t h;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint16_t h0, h1, l0, l1;
-      ns_split(TALL ? s_t[r][c8 + 2 * j] : s_t[c8 + 2 * j][r], h0, l0);
-      ns_split(TALL ? s_t[r][c8 + 2 * j + 1] : s_t[c8 + 2 * j + 1][r], h1, l1);
-      h[j] = h0 | (static_cast<uint32_t>(h1) << 16);
-      l[j] = l0 | (static_cast<uint32_t>(l1) << 16);
-    }
-    const int64_t at = (int64_t)b * cp * rp + (y0 + r) * rp + x0 + c8;
-    *reinterpret_cast<u32x4_t*>(yhi + at) = h;
-    *reinterpret_cast<u32x4_t*>(ylo + at) = l;
+    for (int j = 0; j < 4; ++j)
+      h[j] = f32_to_f16_bits(at(r, c8 + 2 * j)) |
+             (static_cast<uint32_t>(f32_to_f16_bits(at(r, c8 + 2 * j + 1))) << 16);
+    *reinterpret_cast<u32x4_t*>(yhi + (int64_t)b * cp * rp + (y0 + r) * rp + x0 + c8) = h;
+  }
+  // lo: a wave takes one 16 x 16 block at a time, its lanes as the update's
+  for (int i = tid; i < 64 * 16; i += kNsThreads) {
+    const int blk = i >> 6, l = i & 63;
+    const int r = (blk >> 2) * 16 + (l & 15), c = (blk & 3) * 16 + (l >> 4) * 4;
+    uint32_t h, q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ns_split(at(r, c + j), h, q[j]);
+    ylo[b * lo_size + ns_lo_place(static_cast<int>(y0) + r, static_cast<int>(x0) + c, w, tiles_n)] =
+        u32x2_t{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
   }
 }
 
@@ -170,16 +190,16 @@ enum NsMode : int { kGram = 0, kSquare = 1, kUpdate = 2, kOutTall = 3, kOutWide 
 
 struct NsArgs {
   const uint16_t* y;   // (B, cp, rp) hi
-  uint16_t* ylo;       // (B, cp, rp) lo, updated in place
+  u32x2_t* ylo;        // lo of each matrix in the order of ns_lo_place, updated in place
+  int64_t lo_size;     // places of it per matrix
   uint16_t* ynext;     // (B, cp, rp) hi of the next step
   uint16_t* gram;      // (B, rp, rp) A
-  uint16_t* q;         // (B, rp, rp) Q
+  uint16_t* q;         // (B, rp, rp) Q~
   uint16_t* out;       // (B, m, n)
   int cp, rp;
   int om, on;          // m, n: rows and columns of the output
   int tiles_m, tiles_n, tiles;  // tiles per matrix (symmetric products: the upper triangle)
   float a, b, c;       // this step's coefficients
-  float diag;          // added to Q's diagonal (a in the last step)
   float scale;
   int out_bf16;
 };
@@ -228,12 +248,16 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
   int t = lt - b * p.tiles;
   int tm, tn;
   if constexpr (SYM) {
-    tm = 0;
-    while (t >= p.tiles_n - tm) {
-      t -= p.tiles_n - tm;
-      ++tm;
-    }
-    tn = tm + t;
+    // row tm of the upper triangle starts at tile tm * (2 n + 1 - tm) / 2: the
+    // root of that, then corrected (a loop over the rows took 800 cycles)
+    const int n2 = 2 * p.tiles_n + 1;
+    const float d = static_cast<float>(n2);
+    tm = static_cast<int>((d - __builtin_sqrtf(d * d - 8.f * static_cast<float>(t))) * 0.5f);
+    tm = tm < 0 ? 0 : tm >= p.tiles_n ? p.tiles_n - 1 : tm;
+    while (tm > 0 && tm * (n2 - tm) / 2 > t) --tm;
+    while ((tm + 1) * (n2 - tm - 1) / 2 <= t) ++tm;
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = tm + t - tm * (n2 - tm) / 2;
   } else {
     tm = t / p.tiles_n;
     tn = t - tm * p.tiles_n;
@@ -347,8 +371,32 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(get(fb, j), get(fa, i), acc[i][j], 0, 0, 0);
   };
 
+  // What the epilogue reads besides the products, loaded ahead of the main loop
+  // (after it, each of these would cost a memory latency with nothing to hide it):
+  // the update's lo, the square's tile of A
+  constexpr int NE = MODE == kUpdate || MODE == kSquare ? F : 0;
+  u32x2_t ext[NE ? NE : 1][NE ? NE : 1];
+  u32x2_t* lo = nullptr;
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s) issue(s);
+  if constexpr (MODE == kUpdate) {
+    lo = p.ylo + b * p.lo_size + (int64_t)(t * 4 + wave) * (F * F * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) ext[i][j] = lo[(i * F + j) * 64];
+  } else if constexpr (MODE == kSquare) {
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) {
+        const int r = row0 + wr + i * 16 + (lane & 15);
+        const int c = col0 + wc + j * 16 + 4 * (lane >> 4);
+        ext[i][j] = u32x2_t{0u, 0u};
+        if (r < p.rp && c < p.rp)
+          ext[i][j] = *reinterpret_cast<const u32x2_t*>(A + (int64_t)r * p.rp + c);
+      }
+  }
   for (int s = 0; s < stages; ++s) {
     // this wave's loads of stage s have landed (those of the stages after it
     // may be in flight: loads complete in order), then every wave's; and every
@@ -404,13 +452,10 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
         } else {
           const int r = row0 + wr + i * 16 + (lane & 15);
           const int c = col0 + wc + j * 16 + 4 * (lane >> 4);
-          u32x2_t av{0u, 0u};
-          if (r < p.rp && c < p.rp)
-            av = *reinterpret_cast<const u32x2_t*>(A + (int64_t)r * p.rp + c);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float g = f16_bits_to_f32((av[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-            v[e] = p.b * g + p.c * (acc[i][j][e] * kSqScale) + (r == c + e ? p.diag * kDiag : 0.f);
+            const float g = f16_bits_to_f32((ext[i][j][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+            v[e] = p.b * g + p.c * (acc[i][j][e] * kSqScale) + (r == c + e ? p.a * kDiag : 0.f);
           }
         }
         stage4(i, j, pack(v[0], v[1]), pack(v[2], v[3]));
@@ -418,55 +463,40 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
     __syncthreads();
     uint16_t* out = (MODE == kGram ? p.gram : p.q) + b * asz;
     store(out, p.rp, p.rp, p.rp);
-    if (tm != tn) {  // the mirrored tile: columns of the staged one as rows
-      for (int q = tid; q < W * (W / 8); q += kNsThreads) {
-        const int r8 = (q / W) * 8, c = q - (q / W) * W;
-        if (col0 + c < p.rp && row0 + r8 < p.rp) {
-          u32x4_t o;
+    if (tm != tn) {
+      // the mirrored tile: transposing reads of the staged one, each lane 8 rows
+      // of one column, stored as 16 bytes of a row of the mirrored tile
+      const int j = lane & 15, g = lane >> 4;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint16_t x = *reinterpret_cast<const MC2_LDS uint16_t*>(smem + (r8 + 2 * e) * PITCH + c * 2);
-            const uint16_t y =
-                *reinterpret_cast<const MC2_LDS uint16_t*>(smem + (r8 + 2 * e + 1) * PITCH + c * 2);
-            o[e] = x | (static_cast<uint32_t>(y) << 16);
-          }
-          *reinterpret_cast<u32x4_t*>(out + (int64_t)(col0 + c) * p.rp + row0 + r8) = o;
-        }
+      for (int q = 0; q < W * W / 2048; ++q) {  // 16 columns by 32 rows per wave and pass
+        const int id = q * 4 + wave;
+        const int c0 = (id % (W / 16)) * 16, r8 = (id / (W / 16)) * 32 + g * 8;
+        const uint32_t at = s0 + (r8 + (j >> 2)) * PITCH + (c0 + (j & 3) * 4) * 2;
+        u32x2_t h0, h1;
+        asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%3\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(h0), "=&v"(h1) : "v"(at), "i"(4 * PITCH) : "memory");
+        if (col0 + c0 + j < p.rp && row0 + r8 < p.rp)
+          *reinterpret_cast<u32x4_t*>(out + (int64_t)(col0 + c0 + j) * p.rp + row0 + r8) =
+              u32x4_t{h0[0], h0[1], h1[0], h1[1]};
       }
     }
   } else if constexpr (MODE == kUpdate) {
-    uint16_t* lo = p.ylo + b * ysz;
-    u32x2_t keep[F][F];
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
       for (int j = 0; j < F; ++j) {
-        const int r = row0 + wr + i * 16 + (lane & 15);
-        const int c = col0 + wc + j * 16 + 4 * (lane >> 4);
-        u32x2_t hv{0u, 0u}, lv{0u, 0u};
-        if (r < p.cp && c < p.rp) {
-          hv = *reinterpret_cast<const u32x2_t*>(Y + (int64_t)r * p.rp + c);
-          lv = *reinterpret_cast<const u32x2_t*>(lo + (int64_t)r * p.rp + c);
-        }
-        uint16_t h[4], l[4];
+        uint32_t h[4], l[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = f16_bits_to_f32((hv[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) +
-                          f16_bits_to_f32((lv[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * (1.f / kLoScale);
-          ns_split(p.a * x + acc[i][j][e] * kUpdScale, h[e], l[e]);
+          const float rest = f16_bits_to_f32((ext[i][j][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+          ns_split(acc[i][j][e] * kUpdScale + p.a * (1.f / kLoScale) * rest, h[e], l[e]);
         }
-        stage4(i, j, h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16));
-        keep[i][j] = u32x2_t{l[0] | ((uint32_t)l[1] << 16), l[2] | ((uint32_t)l[3] << 16)};
+        stage4(i, j, h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        lo[(i * F + j) * 64] = u32x2_t{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
       }
     __syncthreads();
     store(p.ynext + b * ysz, p.rp, p.cp, p.rp);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int j = 0; j < F; ++j) stage4(i, j, keep[i][j][0], keep[i][j][1]);
-    __syncthreads();
-    store(lo, p.rp, p.cp, p.rp);
   } else {
     const float sc = p.scale * kOutScale;
 #pragma unroll
@@ -750,11 +780,13 @@ static NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
   L.cp = (L.c + kNsPad - 1) / kNsPad * kNsPad;
   const size_t y = static_cast<size_t>(batch * L.cp * L.rp) * 2;  // multiples of 8 KiB
   const size_t a = static_cast<size_t>(batch * L.rp * L.rp) * 2;
+  // lo in whole tiles of up to 128 x 128
+  const size_t l = static_cast<size_t>(batch * ((L.cp + 127) / 128) * ((L.rp + 127) / 128)) * 128 * 128 * 2;
   L.part = 0;
   L.y0 = (static_cast<size_t>(batch) * kNsMaxPart * sizeof(double) + 255) / 256 * 256;
   L.y1 = L.y0 + y;
   L.lo = L.y1 + y;
-  L.gram = L.lo + y;
+  L.gram = L.lo + l;
   L.q = L.gram + a;
   L.total = L.q + a;
   return L;
@@ -762,7 +794,8 @@ static NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
 
 template <int D>
 static void ns_start(const void* g, int64_t batch, int64_t m, int64_t n, const NsLayout& L,
-                     float eps, double* part, uint16_t* y, uint16_t* lo, hipStream_t stream) {
+                     float eps, double* part, uint16_t* y, const NsArgs& p, int w,
+                     hipStream_t stream) {
   const int64_t mn = m * n;
   constexpr int per16 = D == MC2_F32 ? 4 : 8;
   int64_t nb = (mn + kNsThreads * 32 - 1) / (kNsThreads * 32);
@@ -776,33 +809,32 @@ static void ns_start(const void* g, int64_t batch, int64_t m, int64_t n, const N
   static_assert(per16 == 4 || per16 == 8, "16-byte pieces");
   auto init = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, gi, blk, 0, stream, g, m, n, part, static_cast<int>(nb), eps, L.cp,
-                       L.rp, y, lo);
+                       L.rp, y, p.ylo, p.lo_size, w, static_cast<int>((L.rp + w - 1) / w));
   };
   if (m >= n) rows16 ? init(ns_init_kernel<D, true, true>) : init(ns_init_kernel<D, true, false>);
   else rows16 ? init(ns_init_kernel<D, false, true>) : init(ns_init_kernel<D, false, false>);
 }
 
+// Width of a product's tiles: 128 where those fill the chip, else 64.
 template <int MODE>
-static void ns_product(NsArgs p, int64_t batch, hipStream_t stream) {
+static int ns_plan(NsArgs& p, int64_t batch) {
   constexpr bool SYM = MODE == kGram || MODE == kSquare;
   const int rows = MODE == kUpdate || MODE == kOutTall ? p.cp : p.rp;
   const int cols = MODE == kOutWide ? p.cp : p.rp;
-  auto plan = [&](int w) {
+  for (int w = 128;; w = 64) {
     p.tiles_m = (rows + w - 1) / w;
     p.tiles_n = (cols + w - 1) / w;
     p.tiles = SYM ? p.tiles_n * (p.tiles_n + 1) / 2 : p.tiles_m * p.tiles_n;
-    return batch * p.tiles;
-  };
-  // 128 x 128 tiles where they fill the chip, else 64 x 64
-  int64_t grid = plan(128);
-  if (grid >= num_cus()) {
-    hipLaunchKernelGGL((ns_gemm_kernel<128, MODE>), dim3(static_cast<unsigned>(grid)),
-                       dim3(kNsThreads), 0, stream, p);
-  } else {
-    grid = plan(64);
-    hipLaunchKernelGGL((ns_gemm_kernel<64, MODE>), dim3(static_cast<unsigned>(grid)),
-                       dim3(kNsThreads), 0, stream, p);
+    if (w == 64 || batch * p.tiles >= num_cus()) return w;
   }
+}
+
+template <int MODE>
+static void ns_product(NsArgs p, int64_t batch, hipStream_t stream) {
+  const int w = ns_plan<MODE>(p, batch);
+  const dim3 grid(static_cast<unsigned>(batch * p.tiles)), blk(kNsThreads);
+  if (w == 128) hipLaunchKernelGGL((ns_gemm_kernel<128, MODE>), grid, blk, 0, stream, p);
+  else hipLaunchKernelGGL((ns_gemm_kernel<64, MODE>), grid, blk, 0, stream, p);
 }
 
 // The whole call as one launch, for matrices that one workgroup can hold.
@@ -867,17 +899,18 @@ extern "C" int mc2_ns_orthogonalize(const void* g, int64_t batch, int64_t m, int
   char* ws = static_cast<char*>(workspace);
   double* part = reinterpret_cast<double*>(ws + L.part);
   uint16_t* y[2] = {reinterpret_cast<uint16_t*>(ws + L.y0), reinterpret_cast<uint16_t*>(ws + L.y1)};
-  uint16_t* lo = reinterpret_cast<uint16_t*>(ws + L.lo);
-  if (in_dtype == MC2_F32) ns_start<MC2_F32>(g, batch, m, n, L, eps, part, y[0], lo, stream);
-  else if (in_dtype == MC2_BF16) ns_start<MC2_BF16>(g, batch, m, n, L, eps, part, y[0], lo, stream);
-  else ns_start<MC2_F16>(g, batch, m, n, L, eps, part, y[0], lo, stream);
   NsArgs p{};
-  p.ylo = lo;
+  p.cp = static_cast<int>(L.cp);
+  p.rp = static_cast<int>(L.rp);
+  p.ylo = reinterpret_cast<u32x2_t*>(ws + L.lo);
+  const int w = ns_plan<kUpdate>(p, batch);  // lo's order is that of the update's tiles
+  p.lo_size = static_cast<int64_t>(p.tiles) * w * w / 4;
+  if (in_dtype == MC2_F32) ns_start<MC2_F32>(g, batch, m, n, L, eps, part, y[0], p, w, stream);
+  else if (in_dtype == MC2_BF16) ns_start<MC2_BF16>(g, batch, m, n, L, eps, part, y[0], p, w, stream);
+  else ns_start<MC2_F16>(g, batch, m, n, L, eps, part, y[0], p, w, stream);
   p.gram = reinterpret_cast<uint16_t*>(ws + L.gram);
   p.q = reinterpret_cast<uint16_t*>(ws + L.q);
   p.out = static_cast<uint16_t*>(out);
-  p.cp = static_cast<int>(L.cp);
-  p.rp = static_cast<int>(L.rp);
   p.om = static_cast<int>(m);
   p.on = static_cast<int>(n);
   p.scale = scale;
@@ -889,7 +922,6 @@ extern "C" int mc2_ns_orthogonalize(const void* g, int64_t batch, int64_t m, int
     p.a = coeffs[3 * s];
     p.b = coeffs[3 * s + 1];
     p.c = coeffs[3 * s + 2];
-    p.diag = last ? p.a : 0.f;
     ns_product<kGram>(p, batch, stream);
     ns_product<kSquare>(p, batch, stream);
     if (!last) ns_product<kUpdate>(p, batch, stream);
