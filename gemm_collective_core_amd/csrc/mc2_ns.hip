@@ -24,8 +24,7 @@
 // and errors are 1e-3 to 2.5e-3 whatever the rank. The last step leaves lo
 // out, since what it loses is not multiplied again.
 #include "../../include/mc2_train.h"
-#include "gemm_core.hpp"
-#include "mc2_host.hpp"
+#include "mc2_tiles.hpp"
 
 namespace mc2 {
 
@@ -186,6 +185,8 @@ __global__ __launch_bounds__(kNsThreads) void ns_init_kernel(
 
 // ---------------------------------------------------------------- products
 
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 enum NsMode : int { kGram = 0, kSquare = 1, kUpdate = 2, kOutTall = 3, kOutWide = 4 };
 
 struct NsArgs {
@@ -212,12 +213,168 @@ __device__ __forceinline__ int ns_xcd_tile(int b, int n) {
   return x * q + (x < rest ? x : rest) + (b >> 3);
 }
 
+// This workgroup's tile: matrix b, tile t of it, at row tm and column tn of tiles.
+struct NsTile {
+  int b, t, tm, tn;
+};
+template <bool SYM>
+__device__ __forceinline__ NsTile ns_tile(const NsArgs& p) {
+  const int lt = ns_xcd_tile(blockIdx.x, gridDim.x);
+  const int b = uni(lt / p.tiles);
+  const int t = lt - b * p.tiles;
+  if constexpr (SYM) {
+    // row tm of the upper triangle starts at tile tm * (2 n + 1 - tm) / 2: the
+    // root of that, then corrected (a loop over the rows took 800 cycles)
+    const int n2 = 2 * p.tiles_n + 1;
+    const float d = static_cast<float>(n2);
+    int tm = static_cast<int>((d - __builtin_sqrtf(d * d - 8.f * static_cast<float>(t))) * 0.5f);
+    tm = tm < 0 ? 0 : tm >= p.tiles_n ? p.tiles_n - 1 : tm;
+    while (tm > 0 && tm * (n2 - tm) / 2 > t) --tm;
+    while ((tm + 1) * (n2 - tm - 1) / 2 <= t) ++tm;
+    tm = uni(tm);
+    return {b, t, tm, tm + t - tm * (n2 - tm) / 2};
+  } else {
+    const int tm = uni(t / p.tiles_n);
+    return {b, t, tm, t - tm * p.tiles_n};
+  }
+}
+
 // Swizzle of the 32-byte pairs (16 columns) of k row kr in a k-major stage W
 // columns wide: the 16 k rows that one transposing read touches then fall on
 // different banks. It depends on bits 0, 1 and 3 of kr only.
 template <int W>
 __device__ __forceinline__ int ns_kswz(int kr) {
   return W == 128 ? (kr & 3) | (((kr >> 3) & 1) << 2) : ((kr >> 1) & 1) | (((kr >> 3) & 1) << 1);
+}
+
+// This lane's place in lo of its tile (ns_lo_place)
+__device__ __forceinline__ u32x2_t* ns_lo(const NsArgs& p, const NsTile& tl, int f) {
+  return p.ylo + tl.b * p.lo_size + (int64_t)(tl.t * 4 + (threadIdx.x >> 6)) * (f * f * 64) +
+         (threadIdx.x & 63);
+}
+
+// Everything after the products of a W x W tile, held as F x F blocks of
+// accumulators per wave (2 x 2 waves; a lane has four consecutive columns of
+// one row), staged through `smem` for whole-row stores. ext(i, j): the block's
+// four values of A (square) or lo (update), asked for in order.
+template <int W, int MODE, int F, class Ext>
+__device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, lds_t* smem,
+                                            const f32x4_t (&acc)[F][F], Ext&& ext) {
+  constexpr bool SYM = MODE == kGram || MODE == kSquare;
+  constexpr int PITCH = W * 2 + 16;
+  int tid;
+  asm volatile("v_mov_b32 %0, %1" : "=v"(tid) : "v"(static_cast<int>(threadIdx.x)));
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int b = tl.b, tm = tl.tm, tn = tl.tn, row0 = tm * W, col0 = tn * W;
+  const int wr = (wave >> 1) * (W / 2), wc = (wave & 1) * (W / 2);
+  const int64_t ysz = (int64_t)p.cp * p.rp, asz = (int64_t)p.rp * p.rp;
+  const uint32_t s0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
+  auto stage4 = [&](int i, int j, uint32_t x, uint32_t y) {
+    *reinterpret_cast<MC2_LDS u32x2_t*>(smem + (wr + i * 16 + (lane & 15)) * PITCH +
+                                (wc + j * 16 + 4 * (lane >> 4)) * 2) = u32x2_t{x, y};
+  };
+  auto pack = [](float x, float y) {
+    return f32_to_f16_bits(x) | (static_cast<uint32_t>(f32_to_f16_bits(y)) << 16);
+  };
+  // the staged tile -> rows row0 .., columns col0 .. of a matrix of `rows`
+  // rows of `ld` values, 16 bytes at a time (rows are whole pieces)
+  auto store = [&](uint16_t* out, int ld, int rows, int cols) {
+    for (int q = tid; q < W * (W / 8); q += kNsThreads) {
+      const int r = q / (W / 8), c8 = (q - r * (W / 8)) * 8;
+      if (row0 + r < rows && col0 + c8 < cols)
+        *reinterpret_cast<u32x4_t*>(out + (int64_t)(row0 + r) * ld + col0 + c8) =
+            *reinterpret_cast<const MC2_LDS u32x4_t*>(smem + r * PITCH + c8 * 2);
+    }
+  };
+
+  if constexpr (SYM) {
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) {
+        float v[4];
+        if constexpr (MODE == kGram) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e] * kGramScale;
+        } else {
+          const int r = row0 + wr + i * 16 + (lane & 15);
+          const int c = col0 + wc + j * 16 + 4 * (lane >> 4);
+          const u32x2_t x = ext(i, j);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float g = f16_bits_to_f32((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+            v[e] = p.b * g + p.c * (acc[i][j][e] * kSqScale) + (r == c + e ? p.a * kDiag : 0.f);
+          }
+        }
+        stage4(i, j, pack(v[0], v[1]), pack(v[2], v[3]));
+      }
+    __syncthreads();
+    uint16_t* out = (MODE == kGram ? p.gram : p.q) + b * asz;
+    store(out, p.rp, p.rp, p.rp);
+    if (tm != tn) {
+      // the mirrored tile: transposing reads of the staged one, each lane 8 rows
+      // of one column, stored as 16 bytes of a row of the mirrored tile
+      const int j = lane & 15, g = lane >> 4;
+#pragma unroll
+      for (int q = 0; q < W * W / 2048; ++q) {  // 16 columns by 32 rows per wave and pass
+        const int id = q * 4 + wave;
+        const int c0 = (id % (W / 16)) * 16, r8 = (id / (W / 16)) * 32 + g * 8;
+        const uint32_t at = s0 + (r8 + (j >> 2)) * PITCH + (c0 + (j & 3) * 4) * 2;
+        u32x2_t h0, h1;
+        asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%3\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(h0), "=&v"(h1) : "v"(at), "i"(4 * PITCH) : "memory");
+        if (col0 + c0 + j < p.rp && row0 + r8 < p.rp)
+          *reinterpret_cast<u32x4_t*>(out + (int64_t)(col0 + c0 + j) * p.rp + row0 + r8) =
+              u32x4_t{h0[0], h0[1], h1[0], h1[1]};
+      }
+    }
+  } else if constexpr (MODE == kUpdate) {
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) {
+        uint32_t h[4], l[4];
+        const u32x2_t x = ext(i, j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float rest = f16_bits_to_f32((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+          ns_split(acc[i][j][e] * kUpdScale + p.a * (1.f / kLoScale) * rest, h[e], l[e]);
+        }
+        stage4(i, j, h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        ns_lo(p, tl, F)[(i * F + j) * 64] = u32x2_t{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
+      }
+    __syncthreads();
+    store(p.ynext + b * ysz, p.rp, p.cp, p.rp);
+  } else {
+    const float sc = p.scale * kOutScale;
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) {
+        uint32_t w[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = acc[i][j][2 * e] * sc, y = acc[i][j][2 * e + 1] * sc;
+          w[e] = p.out_bf16 ? f32_to_bf16_bits(x) | (static_cast<uint32_t>(f32_to_bf16_bits(y)) << 16)
+                            : pack(x, y);
+        }
+        stage4(i, j, w[0], w[1]);
+      }
+    __syncthreads();
+    uint16_t* out = p.out + (int64_t)b * p.om * p.on;
+    if (p.on % 8 == 0) {
+      store(out, p.on, p.om, p.on);
+    } else {  // rows that are not whole 16-byte pieces
+      for (int q = tid; q < W * W; q += kNsThreads) {
+        const int r = q / W, c = q - r * W;
+        if (row0 + r < p.om && col0 + c < p.on)
+          out[(int64_t)(row0 + r) * p.on + col0 + c] =
+              *reinterpret_cast<const MC2_LDS uint16_t*>(smem + r * PITCH + c * 2);
+      }
+    }
+  }
 }
 
 // One W x W tile of a product. 4 waves as 2 x 2; K in stages of 64 through a
@@ -243,25 +400,8 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int lt = ns_xcd_tile(blockIdx.x, gridDim.x);
-  const int b = lt / p.tiles;
-  int t = lt - b * p.tiles;
-  int tm, tn;
-  if constexpr (SYM) {
-    // row tm of the upper triangle starts at tile tm * (2 n + 1 - tm) / 2: the
-    // root of that, then corrected (a loop over the rows took 800 cycles)
-    const int n2 = 2 * p.tiles_n + 1;
-    const float d = static_cast<float>(n2);
-    tm = static_cast<int>((d - __builtin_sqrtf(d * d - 8.f * static_cast<float>(t))) * 0.5f);
-    tm = tm < 0 ? 0 : tm >= p.tiles_n ? p.tiles_n - 1 : tm;
-    while (tm > 0 && tm * (n2 - tm) / 2 > t) --tm;
-    while ((tm + 1) * (n2 - tm - 1) / 2 <= t) ++tm;
-    tm = __builtin_amdgcn_readfirstlane(tm);
-    tn = tm + t - tm * (n2 - tm) / 2;
-  } else {
-    tm = t / p.tiles_n;
-    tn = t - tm * p.tiles_n;
-  }
+  const NsTile tl = ns_tile<SYM>(p);
+  const int b = tl.b, t = tl.t, tm = tl.tm, tn = tl.tn;
   const int row0 = tm * W, col0 = tn * W;
   const int64_t ysz = (int64_t)p.cp * p.rp, asz = (int64_t)p.rp * p.rp;
   const uint16_t* Y = p.y + b * ysz;
@@ -376,11 +516,10 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
   // the update's lo, the square's tile of A
   constexpr int NE = MODE == kUpdate || MODE == kSquare ? F : 0;
   u32x2_t ext[NE ? NE : 1][NE ? NE : 1];
-  u32x2_t* lo = nullptr;
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s) issue(s);
   if constexpr (MODE == kUpdate) {
-    lo = p.ylo + b * p.lo_size + (int64_t)(t * 4 + wave) * (F * F * 64) + lane;
+    const u32x2_t* lo = ns_lo(p, tl, F);
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
@@ -422,109 +561,66 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
   wait_vmcnt0();
   __syncthreads();  // every read of the operands is done: their place takes the output
 
-  auto stage4 = [&](int i, int j, uint32_t x, uint32_t y) {
-    *reinterpret_cast<MC2_LDS u32x2_t*>(smem + (wr + i * 16 + (lane & 15)) * PITCH +
-                                (wc + j * 16 + 4 * (lane >> 4)) * 2) = u32x2_t{x, y};
-  };
-  auto pack = [](float x, float y) {
-    return f32_to_f16_bits(x) | (static_cast<uint32_t>(f32_to_f16_bits(y)) << 16);
-  };
-  // the staged tile -> rows row0 .., columns col0 .. of a matrix of `rows`
-  // rows of `ld` values, 16 bytes at a time (rows are whole pieces)
-  auto store = [&](uint16_t* out, int ld, int rows, int cols) {
-    for (int q = tid; q < W * (W / 8); q += kNsThreads) {
-      const int r = q / (W / 8), c8 = (q - r * (W / 8)) * 8;
-      if (row0 + r < rows && col0 + c8 < cols)
-        *reinterpret_cast<u32x4_t*>(out + (int64_t)(row0 + r) * ld + col0 + c8) =
-            *reinterpret_cast<const MC2_LDS u32x4_t*>(smem + r * PITCH + c8 * 2);
-    }
-  };
+  ns_epilogue<W, MODE, F>(p, tl, smem, acc, [&](int i, int j) { return ext[NE ? i : 0][NE ? j : 0]; });
+}
 
-  if constexpr (SYM) {
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int j = 0; j < F; ++j) {
-        float v[4];
-        if constexpr (MODE == kGram) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e] * kGramScale;
-        } else {
-          const int r = row0 + wr + i * 16 + (lane & 15);
-          const int c = col0 + wc + j * 16 + 4 * (lane >> 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float g = f16_bits_to_f32((ext[i][j][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-            v[e] = p.b * g + p.c * (acc[i][j][e] * kSqScale) + (r == c + e ? p.a * kDiag : 0.f);
-          }
-        }
-        stage4(i, j, pack(v[0], v[1]), pack(v[2], v[3]));
-      }
-    __syncthreads();
-    uint16_t* out = (MODE == kGram ? p.gram : p.q) + b * asz;
-    store(out, p.rp, p.rp, p.rp);
-    if (tm != tn) {
-      // the mirrored tile: transposing reads of the staged one, each lane 8 rows
-      // of one column, stored as 16 bytes of a row of the mirrored tile
-      const int j = lane & 15, g = lane >> 4;
-#pragma unroll
-      for (int q = 0; q < W * W / 2048; ++q) {  // 16 columns by 32 rows per wave and pass
-        const int id = q * 4 + wave;
-        const int c0 = (id % (W / 16)) * 16, r8 = (id / (W / 16)) * 32 + g * 8;
-        const uint32_t at = s0 + (r8 + (j >> 2)) * PITCH + (c0 + (j & 3) * 4) * 2;
-        u32x2_t h0, h1;
-        asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%3\n\t"
-                     "s_waitcnt lgkmcnt(0)"
-                     : "=&v"(h0), "=&v"(h1) : "v"(at), "i"(4 * PITCH) : "memory");
-        if (col0 + c0 + j < p.rp && row0 + r8 < p.rp)
-          *reinterpret_cast<u32x4_t*>(out + (int64_t)(col0 + c0 + j) * p.rp + row0 + r8) =
-              u32x4_t{h0[0], h0[1], h1[0], h1[1]};
-      }
-    }
-  } else if constexpr (MODE == kUpdate) {
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int j = 0; j < F; ++j) {
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float rest = f16_bits_to_f32((ext[i][j][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-          ns_split(acc[i][j][e] * kUpdScale + p.a * (1.f / kLoScale) * rest, h[e], l[e]);
-        }
-        stage4(i, j, h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-        lo[(i * F + j) * 64] = u32x2_t{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
-      }
-    __syncthreads();
-    store(p.ynext + b * ysz, p.rp, p.cp, p.rp);
+// One 256 x 256 tile on the four-wave main loop (gemm_core_w4.hpp), whose waves
+// of 128 x 128 read half as much LDS per product as the 128 x 128 tiles' waves:
+// those are bound by LDS bandwidth. One workgroup per CU.
+template <int MODE>
+__global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
+  constexpr bool SYM = MODE == kGram || MODE == kSquare;
+  constexpr int F = TileW::FM;
+  static_assert(TileW::BM == 256 && TileW::BN == 256 && TileW::FN == F && TileW::NT == kNsThreads,
+                "2 x 2 waves of 128 x 128");
+  constexpr int kStage = 256 * (256 * 2 + 16), kRing = TileW::kStages * TileW::kStageBytes;
+  __shared__ __attribute__((aligned(16))) char smem_raw[kStage > kRing ? kStage : kRing];
+  lds_t* smem = (lds_t*)smem_raw;
+  const NsTile tl = ns_tile<SYM>(p);
+  const int row0 = tl.tm * 256, col0 = tl.tn * 256;
+  const int64_t ysz = (int64_t)p.cp * p.rp, asz = (int64_t)p.rp * p.rp;
+  const char* Y = reinterpret_cast<const char*>(p.y + tl.b * ysz);
+  const char* A = reinterpret_cast<const char*>(p.gram + tl.b * asz);
+  const char* Q = reinterpret_cast<const char*>(p.q + tl.b * asz);
+  const int64_t ld = (int64_t)p.rp * 2;
+  const int na = MODE == kUpdate || MODE == kOutTall ? p.cp : p.rp;
+  const int nb = MODE == kOutWide ? p.cp : p.rp;
+  const int k = MODE == kGram ? p.cp : p.rp;
+  const KSpan ks{k, 0, 0, k / 64, k / 64};
+  f32x4_t acc[F][F];
+  if constexpr (MODE == kGram) {
+    mainloop_w4<Elem::F16, false, TileW, false, true>(smem, Y, ld, row0, na - 1, BDesc{Y, ld, nb},
+                                                      col0, PlainCols{col0, nb - 8}, ks, acc);
   } else {
-    const float sc = p.scale * kOutScale;
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int j = 0; j < F; ++j) {
-        uint32_t w[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = acc[i][j][2 * e] * sc, y = acc[i][j][2 * e + 1] * sc;
-          w[e] = p.out_bf16 ? f32_to_bf16_bits(x) | (static_cast<uint32_t>(f32_to_bf16_bits(y)) << 16)
-                            : pack(x, y);
-        }
-        stage4(i, j, w[0], w[1]);
-      }
-    __syncthreads();
-    uint16_t* out = p.out + (int64_t)b * p.om * p.on;
-    if (p.on % 8 == 0) {
-      store(out, p.on, p.om, p.on);
-    } else {  // rows that are not whole 16-byte pieces
-      for (int q = tid; q < W * W; q += kNsThreads) {
-        const int r = q / W, c = q - r * W;
-        if (row0 + r < p.om && col0 + c < p.on)
-          out[(int64_t)(row0 + r) * p.on + col0 + c] =
-              *reinterpret_cast<const MC2_LDS uint16_t*>(smem + r * PITCH + c * 2);
-      }
-    }
+    const char* a = MODE == kSquare ? A : MODE == kOutWide ? Q : Y;
+    const char* b = MODE == kSquare ? A : MODE == kOutWide ? Y : Q;
+    mainloop_w4<Elem::F16, true, TileW, false>(smem, a, ld, row0, na - 1, BDesc{b, ld, nb}, col0,
+                                               PlainCols{col0, nb - 8}, ks, acc);
   }
+  // The epilogue's other operand, one row of blocks ahead of its use (the
+  // accumulators leave no room to hold it through the main loop).
+  u32x2_t ext[2][F];
+  auto load = [&](int i) {
+    if constexpr (MODE == kUpdate) {
+      const u32x2_t* lo = ns_lo(p, tl, F);
+#pragma unroll
+      for (int j = 0; j < F; ++j) ext[i & 1][j] = lo[(i * F + j) * 64];
+    } else if constexpr (MODE == kSquare) {
+      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+      const int r = row0 + (wave >> 1) * 128 + i * 16 + (lane & 15);
+      const int c0 = col0 + (wave & 1) * 128 + 4 * (lane >> 4);
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+        ext[i & 1][j] = r < p.rp && c0 + j * 16 < p.rp
+                            ? *reinterpret_cast<const u32x2_t*>(A + r * ld + (c0 + j * 16) * 2)
+                            : u32x2_t{0u, 0u};
+    }
+  };
+  load(0);
+  ns_epilogue<256, MODE, F>(p, tl, smem, acc, [&](int i, int j) {
+    if (j == 0 && i + 1 < F) load(i + 1);
+    return ext[i & 1][j];
+  });
 }
 
 // ---------------------------------------------------------------- one workgroup per matrix
@@ -780,8 +876,8 @@ static NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
   L.cp = (L.c + kNsPad - 1) / kNsPad * kNsPad;
   const size_t y = static_cast<size_t>(batch * L.cp * L.rp) * 2;  // multiples of 8 KiB
   const size_t a = static_cast<size_t>(batch * L.rp * L.rp) * 2;
-  // lo in whole tiles of up to 128 x 128
-  const size_t l = static_cast<size_t>(batch * ((L.cp + 127) / 128) * ((L.rp + 127) / 128)) * 128 * 128 * 2;
+  // lo in whole tiles of up to 256 x 256
+  const size_t l = static_cast<size_t>(batch * ((L.cp + 255) / 256) * ((L.rp + 255) / 256)) * 256 * 256 * 2;
   L.part = 0;
   L.y0 = (static_cast<size_t>(batch) * kNsMaxPart * sizeof(double) + 255) / 256 * 256;
   L.y1 = L.y0 + y;
@@ -815,13 +911,13 @@ static void ns_start(const void* g, int64_t batch, int64_t m, int64_t n, const N
   else rows16 ? init(ns_init_kernel<D, false, true>) : init(ns_init_kernel<D, false, false>);
 }
 
-// Width of a product's tiles: 128 where those fill the chip, else 64.
+// Width of a product's tiles: the widest that gives every CU one.
 template <int MODE>
 static int ns_plan(NsArgs& p, int64_t batch) {
   constexpr bool SYM = MODE == kGram || MODE == kSquare;
   const int rows = MODE == kUpdate || MODE == kOutTall ? p.cp : p.rp;
   const int cols = MODE == kOutWide ? p.cp : p.rp;
-  for (int w = 128;; w = 64) {
+  for (int w = 256;; w /= 2) {
     p.tiles_m = (rows + w - 1) / w;
     p.tiles_n = (cols + w - 1) / w;
     p.tiles = SYM ? p.tiles_n * (p.tiles_n + 1) / 2 : p.tiles_m * p.tiles_n;
@@ -833,7 +929,8 @@ template <int MODE>
 static void ns_product(NsArgs p, int64_t batch, hipStream_t stream) {
   const int w = ns_plan<MODE>(p, batch);
   const dim3 grid(static_cast<unsigned>(batch * p.tiles)), blk(kNsThreads);
-  if (w == 128) hipLaunchKernelGGL((ns_gemm_kernel<128, MODE>), grid, blk, 0, stream, p);
+  if (w == 256) hipLaunchKernelGGL(ns_gemm256_kernel<MODE>, grid, blk, 0, stream, p);
+  else if (w == 128) hipLaunchKernelGGL((ns_gemm_kernel<128, MODE>), grid, blk, 0, stream, p);
   else hipLaunchKernelGGL((ns_gemm_kernel<64, MODE>), grid, blk, 0, stream, p);
 }
 

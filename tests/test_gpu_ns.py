@@ -49,7 +49,9 @@ def _check(g, out, *, coeffs=(CO,) * 5, eps=1e-7, scale=1.0, tol=NS_TOL):
     (5, 100, 72, F16, BF), (8, 264, 272, F32, BF), (1, 272, 264, F32, BF), (3, 129, 130, BF, F16),
     (2, 131, 517, F32, BF), (2, 517, 131, F32, BF), (1, 777, 1001, F32, BF),
     (1, 1001, 777, BF, BF), (16, 384, 256, F32, BF), (2, 512, 1024, F16, F16),
-    (1, 1536, 1537, F32, BF), (3, 24, 1000, F32, BF), (40, 136, 200, F32, BF)])
+    (1, 1536, 1537, F32, BF), (3, 24, 1000, F32, BF), (40, 136, 200, F32, BF),
+    (256, 136, 200, F32, BF), (260, 200, 136, BF, F16), (90, 264, 520, F32, BF),
+    (90, 513, 260, F16, BF)])
 def test_sizes_and_types(B, m, n, dt, out):
     g = torch.randn((B, m, n), generator=torch.Generator().manual_seed(m * 7 + n)).to(dt).cuda()
     keep = g.clone()
