@@ -187,6 +187,8 @@ __global__ __launch_bounds__(kNsThreads) void ns_init_kernel(
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
 enum NsMode : int { kGram = 0, kSquare = 1, kUpdate = 2, kOutTall = 3, kOutWide = 4 };
 
 struct NsArgs {
@@ -253,15 +255,27 @@ __device__ __forceinline__ u32x2_t* ns_lo(const NsArgs& p, const NsTile& tl, int
          (threadIdx.x & 63);
 }
 
+// Place of 16-byte chunk c of row r of a W x W tile of 16-bit values staged in
+// LDS: chunks swizzled in pairs by the row, so that 16 rows of 32 bytes each
+// (what the blocks' lanes write, and what a transposing read takes) spread over
+// the banks.
+template <int W>
+__device__ __forceinline__ int ns_spos(int r, int c) {
+  constexpr int kPairs = W / 16;  // 32-byte pairs per row
+  return r * (W * 2) + ((c ^ ((r & (kPairs - 1)) << 1)) << 4);
+}
+
 // Everything after the products of a W x W tile, held as F x F blocks of
 // accumulators per wave (2 x 2 waves; a lane has four consecutive columns of
 // one row), staged through `smem` for whole-row stores. ext(i, j): the block's
-// four values of A (square) or lo (update), asked for in order.
-template <int W, int MODE, int F, class Ext>
+// four values of lo (update) or, with !A_IN_LDS, of A (square), asked for in
+// order; with A_IN_LDS A's tile lies in `smem` and Q~ takes its place.
+template <int W, int MODE, int F, bool A_IN_LDS, class Ext>
 __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, lds_t* smem,
                                             const f32x4_t (&acc)[F][F], Ext&& ext) {
   constexpr bool SYM = MODE == kGram || MODE == kSquare;
-  constexpr int PITCH = W * 2 + 16;
+  // The thread index through an assembly move: what is derived from it is then
+  // computed here and not kept live through the main loop.
   int tid;
   asm volatile("v_mov_b32 %0, %1" : "=v"(tid) : "v"(static_cast<int>(threadIdx.x)));
   const int lane = tid & 63;
@@ -269,22 +283,33 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
   const int b = tl.b, tm = tl.tm, tn = tl.tn, row0 = tm * W, col0 = tn * W;
   const int wr = (wave >> 1) * (W / 2), wc = (wave & 1) * (W / 2);
   const int64_t ysz = (int64_t)p.cp * p.rp, asz = (int64_t)p.rp * p.rp;
-  const uint32_t s0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
-  auto stage4 = [&](int i, int j, uint32_t x, uint32_t y) {
-    *reinterpret_cast<MC2_LDS u32x2_t*>(smem + (wr + i * 16 + (lane & 15)) * PITCH +
-                                (wc + j * 16 + 4 * (lane >> 4)) * 2) = u32x2_t{x, y};
+  // this lane's four values of block (i, j) in the staged tile
+  auto place = [&](int i, int j) {
+    const int r = wr + i * 16 + (lane & 15), c = wc + j * 16 + 4 * (lane >> 4);
+    return reinterpret_cast<MC2_LDS u32x2_t*>(smem + ns_spos<W>(r, c >> 3) + ((c & 4) << 1));
   };
   auto pack = [](float x, float y) {
     return f32_to_f16_bits(x) | (static_cast<uint32_t>(f32_to_f16_bits(y)) << 16);
   };
   // the staged tile -> rows row0 .., columns col0 .. of a matrix of `rows`
-  // rows of `ld` values, 16 bytes at a time (rows are whole pieces)
+  // rows of `ld` values, 16 bytes at a time (rows are whole pieces), eight LDS
+  // reads in flight per thread
   auto store = [&](uint16_t* out, int ld, int rows, int cols) {
-    for (int q = tid; q < W * (W / 8); q += kNsThreads) {
-      const int r = q / (W / 8), c8 = (q - r * (W / 8)) * 8;
-      if (row0 + r < rows && col0 + c8 < cols)
-        *reinterpret_cast<u32x4_t*>(out + (int64_t)(row0 + r) * ld + col0 + c8) =
-            *reinterpret_cast<const MC2_LDS u32x4_t*>(smem + r * PITCH + c8 * 2);
+    constexpr int N = W * (W / 8) / kNsThreads, U = N < 8 ? N : 8;
+    const int r0 = tid / (W / 8), c8 = tid % (W / 8);
+    constexpr int RS = kNsThreads / (W / 8);  // rows per pass
+    uint16_t* o = out + (int64_t)(row0 + r0) * ld + col0 + c8 * 8;
+    const bool col_in = col0 + c8 * 8 < cols;
+#pragma unroll 1
+    for (int k0 = 0; k0 < N; k0 += U) {
+      u32x4_t v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        v[u] = *reinterpret_cast<const MC2_LDS u32x4_t*>(smem + ns_spos<W>(r0 + (k0 + u) * RS, c8));
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (col_in && row0 + r0 + (k0 + u) * RS < rows)
+          *reinterpret_cast<u32x4_t*>(o + (int64_t)(k0 + u) * RS * ld) = v[u];
     }
   };
 
@@ -300,14 +325,17 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
         } else {
           const int r = row0 + wr + i * 16 + (lane & 15);
           const int c = col0 + wc + j * 16 + 4 * (lane >> 4);
-          const u32x2_t x = ext(i, j);
+          u32x2_t x;
+          if constexpr (A_IN_LDS) x = *place(i, j);
+          else x = ext(i, j);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float g = f16_bits_to_f32((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-            v[e] = p.b * g + p.c * (acc[i][j][e] * kSqScale) + (r == c + e ? p.a * kDiag : 0.f);
+            v[e] = p.b * g + p.c * kSqScale * acc[i][j][e];
+            if (tm == tn) v[e] += r == c + e ? p.a * kDiag : 0.f;
           }
         }
-        stage4(i, j, pack(v[0], v[1]), pack(v[2], v[3]));
+        *place(i, j) = u32x2_t{pack(v[0], v[1]), pack(v[2], v[3])};
       }
     __syncthreads();
     uint16_t* out = (MODE == kGram ? p.gram : p.q) + b * asz;
@@ -316,21 +344,33 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
       // the mirrored tile: transposing reads of the staged one, each lane 8 rows
       // of one column, stored as 16 bytes of a row of the mirrored tile
       const int j = lane & 15, g = lane >> 4;
+      constexpr int U = 4;  // passes with their reads in flight together
+#pragma unroll 1
+      for (int q0 = 0; q0 < W * W / 2048; q0 += W == 64 ? 2 : U) {
+        constexpr int UU = W == 64 ? 2 : U;  // 16 columns by 32 rows per wave and pass
+        u32x2_t h[UU][2];
 #pragma unroll
-      for (int q = 0; q < W * W / 2048; ++q) {  // 16 columns by 32 rows per wave and pass
-        const int id = q * 4 + wave;
-        const int c0 = (id % (W / 16)) * 16, r8 = (id / (W / 16)) * 32 + g * 8;
-        const uint32_t at = s0 + (r8 + (j >> 2)) * PITCH + (c0 + (j & 3) * 4) * 2;
-        u32x2_t h0, h1;
-        asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%3\n\t"
-                     "s_waitcnt lgkmcnt(0)"
-                     : "=&v"(h0), "=&v"(h1) : "v"(at), "i"(4 * PITCH) : "memory");
-        if (col0 + c0 + j < p.rp && row0 + r8 < p.rp)
-          *reinterpret_cast<u32x4_t*>(out + (int64_t)(col0 + c0 + j) * p.rp + row0 + r8) =
-              u32x4_t{h0[0], h0[1], h1[0], h1[1]};
+        for (int u = 0; u < UU; ++u) {
+          const int id = (q0 + u) * 4 + wave;
+          const int c0 = (id % (W / 16)) * 16, kr = (id / (W / 16)) * 32 + g * 8 + (j >> 2);
+          const int c = (c0 >> 3) + ((j & 3) >> 1), in = (j & 1) << 3;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            h[u][k] = bit_cast<u32x2_t>(__builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                reinterpret_cast<MC2_LDS s16x4_t*>(smem + ns_spos<W>(kr + 4 * k, c) + in)));
+        }
+#pragma unroll
+        for (int u = 0; u < UU; ++u) {
+          const int id = (q0 + u) * 4 + wave;
+          const int c = col0 + (id % (W / 16)) * 16 + j, r8 = row0 + (id / (W / 16)) * 32 + g * 8;
+          if (c < p.rp && r8 < p.rp)
+            *reinterpret_cast<u32x4_t*>(out + (int64_t)c * p.rp + r8) =
+                u32x4_t{h[u][0][0], h[u][0][1], h[u][1][0], h[u][1][1]};
+        }
       }
     }
   } else if constexpr (MODE == kUpdate) {
+    u32x2_t* lo = ns_lo(p, tl, F);
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
@@ -342,26 +382,27 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
           const float rest = f16_bits_to_f32((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
           ns_split(acc[i][j][e] * kUpdScale + p.a * (1.f / kLoScale) * rest, h[e], l[e]);
         }
-        stage4(i, j, h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-        ns_lo(p, tl, F)[(i * F + j) * 64] = u32x2_t{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
+        *place(i, j) = u32x2_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+        lo[(i * F + j) * 64] = u32x2_t{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
       }
     __syncthreads();
     store(p.ynext + b * ysz, p.rp, p.cp, p.rp);
   } else {
     const float sc = p.scale * kOutScale;
+    auto stage = [&](auto cvt) {
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+      for (int i = 0; i < F; ++i)
 #pragma unroll
-      for (int j = 0; j < F; ++j) {
-        uint32_t w[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = acc[i][j][2 * e] * sc, y = acc[i][j][2 * e + 1] * sc;
-          w[e] = p.out_bf16 ? f32_to_bf16_bits(x) | (static_cast<uint32_t>(f32_to_bf16_bits(y)) << 16)
-                            : pack(x, y);
-        }
-        stage4(i, j, w[0], w[1]);
-      }
+        for (int j = 0; j < F; ++j)
+          *place(i, j) = u32x2_t{cvt(acc[i][j][0] * sc, acc[i][j][1] * sc),
+                                 cvt(acc[i][j][2] * sc, acc[i][j][3] * sc)};
+    };
+    if (p.out_bf16)
+      stage([](float x, float y) {
+        return f32_to_bf16_bits(x) | (static_cast<uint32_t>(f32_to_bf16_bits(y)) << 16);
+      });
+    else
+      stage(pack);
     __syncthreads();
     uint16_t* out = p.out + (int64_t)b * p.om * p.on;
     if (p.on % 8 == 0) {
@@ -370,8 +411,8 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
       for (int q = tid; q < W * W; q += kNsThreads) {
         const int r = q / W, c = q - r * W;
         if (row0 + r < p.om && col0 + c < p.on)
-          out[(int64_t)(row0 + r) * p.on + col0 + c] =
-              *reinterpret_cast<const MC2_LDS uint16_t*>(smem + r * PITCH + c * 2);
+          out[(int64_t)(row0 + r) * p.on + col0 + c] = *reinterpret_cast<const MC2_LDS uint16_t*>(
+              smem + ns_spos<W>(r, c >> 3) + (c & 7) * 2);
       }
     }
   }
@@ -393,9 +434,8 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
   constexpr int NL = OB / 4096;    // 1 KiB loads per wave, operand and stage
   constexpr int F = W / 32;        // 16-row fragments per wave and operand
   constexpr int NR = KMAJ ? 4 * F : 2 * F;  // LDS reads per wave and k-step
-  constexpr int PITCH = W * 2 + 16;
   __shared__ __attribute__((aligned(16))) char smem_raw[NS * 2 * OB];
-  static_assert(W * PITCH <= NS * 2 * OB, "the output tile is staged in the operands' place");
+  static_assert(W * W * 2 <= NS * 2 * OB, "the output tile is staged in the operands' place");
   lds_t* smem = (lds_t*)smem_raw;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -561,7 +601,7 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
   wait_vmcnt0();
   __syncthreads();  // every read of the operands is done: their place takes the output
 
-  ns_epilogue<W, MODE, F>(p, tl, smem, acc, [&](int i, int j) { return ext[NE ? i : 0][NE ? j : 0]; });
+  ns_epilogue<W, MODE, F, false>(p, tl, smem, acc, [&](int i, int j) { return ext[NE ? i : 0][NE ? j : 0]; });
 }
 
 // One 256 x 256 tile on the four-wave main loop (gemm_core_w4.hpp), whose waves
@@ -573,8 +613,9 @@ __global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
   constexpr int F = TileW::FM;
   static_assert(TileW::BM == 256 && TileW::BN == 256 && TileW::FN == F && TileW::NT == kNsThreads,
                 "2 x 2 waves of 128 x 128");
-  constexpr int kStage = 256 * (256 * 2 + 16), kRing = TileW::kStages * TileW::kStageBytes;
-  __shared__ __attribute__((aligned(16))) char smem_raw[kStage > kRing ? kStage : kRing];
+  static_assert(TileW::kStages * TileW::kStageBytes == 256 * 256 * 2,
+                "the output tile is staged in the operands' place");
+  __shared__ __attribute__((aligned(16))) char smem_raw[256 * 256 * 2];
   lds_t* smem = (lds_t*)smem_raw;
   const NsTile tl = ns_tile<SYM>(p);
   const int row0 = tl.tm * 256, col0 = tl.tn * 256;
@@ -597,29 +638,39 @@ __global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
     mainloop_w4<Elem::F16, true, TileW, false>(smem, a, ld, row0, na - 1, BDesc{b, ld, nb}, col0,
                                                PlainCols{col0, nb - 8}, ks, acc);
   }
-  // The epilogue's other operand, one row of blocks ahead of its use (the
-  // accumulators leave no room to hold it through the main loop).
-  u32x2_t ext[2][F];
+  if constexpr (MODE == kSquare) {
+    // A's tile, straight into the staged tile's places (loads of 8 bytes per
+    // lane from A's rows took 45 k cycles a tile). A load fills two rows; rows
+    // and columns beyond A load zeros.
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const auto ra = make_rsrc(A + row0 * ld);
+#pragma unroll 4
+    for (int i = 0; i < 32; ++i) {
+      const int r = wave * 64 + i * 2 + (lane >> 5);
+      const int c = (lane & 31) ^ ((r & 15) << 1);
+      const bool in = row0 + r < p.rp && col0 + c * 8 < p.rp;
+      dma16(ra, smem + (wave * 32 + i) * 1024,
+            in ? static_cast<uint32_t>(r * ld + (col0 + c * 8) * 2) : kOffNone);
+    }
+    wait_vmcnt0();
+    __syncthreads();
+  }
+  // lo, two rows of blocks ahead of its use (the accumulators leave no room to
+  // hold it through the main loop)
+  u32x2_t ext[3][F];
   auto load = [&](int i) {
     if constexpr (MODE == kUpdate) {
       const u32x2_t* lo = ns_lo(p, tl, F);
 #pragma unroll
-      for (int j = 0; j < F; ++j) ext[i & 1][j] = lo[(i * F + j) * 64];
-    } else if constexpr (MODE == kSquare) {
-      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-      const int r = row0 + (wave >> 1) * 128 + i * 16 + (lane & 15);
-      const int c0 = col0 + (wave & 1) * 128 + 4 * (lane >> 4);
-#pragma unroll
-      for (int j = 0; j < F; ++j)
-        ext[i & 1][j] = r < p.rp && c0 + j * 16 < p.rp
-                            ? *reinterpret_cast<const u32x2_t*>(A + r * ld + (c0 + j * 16) * 2)
-                            : u32x2_t{0u, 0u};
+      for (int j = 0; j < F; ++j) ext[i % 3][j] = lo[(i * F + j) * 64];
     }
   };
   load(0);
-  ns_epilogue<256, MODE, F>(p, tl, smem, acc, [&](int i, int j) {
-    if (j == 0 && i + 1 < F) load(i + 1);
-    return ext[i & 1][j];
+  load(1);
+  ns_epilogue<256, MODE, F, MODE == kSquare>(p, tl, smem, acc, [&](int i, int j) {
+    if (j == 0 && i + 2 < F) load(i + 2);
+    return ext[i % 3][j];
   });
 }
 
@@ -659,8 +710,6 @@ __device__ __forceinline__ f16x8_t tiny_row(const char* s, int r0, int ks) {
   const int lane = threadIdx.x & 63;
   return *reinterpret_cast<const f16x8_t*>(s + tiny_pos<RP>(r0 + (lane & 15), ks * 4 + (lane >> 4)));
 }
-
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 // 16 columns at c0 as a fragment over k rows ks * 32 .. + 31
 template <int RP>
