@@ -202,6 +202,9 @@ struct NsArgs {
   int cp, rp;
   int om, on;          // m, n: rows and columns of the output
   int tiles_m, tiles_n, tiles;  // tiles per matrix (symmetric products: the upper triangle)
+  int row_tiles;                // tiles per row in ns_tile's order
+  float inv_tiles, inv_row_tiles;
+  int keep_lo;                  // the update writes lo (a later update reads it)
   float a, b, c;       // this step's coefficients
   float scale;
   int out_bf16;
@@ -209,7 +212,8 @@ struct NsArgs {
 
 // Tile of workgroup b of n: workgroups go to the 8 XCDs in turn, so XCD x takes
 // the x-th eighth of the tiles, whose rows and columns its L2 then shares (with
-// 8 or 16 matrices, whole matrices).
+// 8 or 16 matrices, whole matrices, and what one launch wrote the next one finds
+// there: 8 x 264 x 272 takes 73 us, with every other launch in reverse order 85).
 __device__ __forceinline__ int ns_xcd_tile(int b, int n) {
   const int x = b & 7, q = n >> 3, rest = n & 7;
   return x * q + (x < rest ? x : rest) + (b >> 3);
@@ -219,25 +223,30 @@ __device__ __forceinline__ int ns_xcd_tile(int b, int n) {
 struct NsTile {
   int b, t, tm, tn;
 };
+// n / d for n < 2^24, with 1 / d at hand: a handful of instructions. (The time
+// from a workgroup's start to its first load is mostly that of fetching its
+// instructions: an integer division and a loop over the triangle's rows took
+// 1500 cycles of it.)
+__device__ __forceinline__ int ns_div(int n, int d, float inv) {
+  int q = static_cast<int>(static_cast<float>(n) * inv);
+  const int r = n - q * d;
+  q += r >= d ? 1 : 0;
+  q -= r < 0 ? 1 : 0;
+  return uni(q);
+}
 template <bool SYM>
 __device__ __forceinline__ NsTile ns_tile(const NsArgs& p) {
   const int lt = ns_xcd_tile(blockIdx.x, gridDim.x);
-  const int b = uni(lt / p.tiles);
+  const int b = ns_div(lt, p.tiles, p.inv_tiles);
   const int t = lt - b * p.tiles;
+  const int tm = ns_div(t, p.row_tiles, p.inv_row_tiles), c = t - tm * p.row_tiles;
   if constexpr (SYM) {
-    // row tm of the upper triangle starts at tile tm * (2 n + 1 - tm) / 2: the
-    // root of that, then corrected (a loop over the rows took 800 cycles)
-    const int n2 = 2 * p.tiles_n + 1;
-    const float d = static_cast<float>(n2);
-    int tm = static_cast<int>((d - __builtin_sqrtf(d * d - 8.f * static_cast<float>(t))) * 0.5f);
-    tm = tm < 0 ? 0 : tm >= p.tiles_n ? p.tiles_n - 1 : tm;
-    while (tm > 0 && tm * (n2 - tm) / 2 > t) --tm;
-    while ((tm + 1) * (n2 - tm - 1) / 2 <= t) ++tm;
-    tm = uni(tm);
-    return {b, t, tm, tm + t - tm * (n2 - tm) / 2};
+    // the upper triangle of n x n tiles folded to rows of n + 1: row i of the
+    // triangle, n - i tiles, and behind it row n - 1 - i, of i + 1 tiles
+    const int n = p.tiles_n, i = n - 1 - tm;
+    return c < n - tm ? NsTile{b, t, tm, tm + c} : NsTile{b, t, i, i + c - (n - tm)};
   } else {
-    const int tm = uni(t / p.tiles_n);
-    return {b, t, tm, t - tm * p.tiles_n};
+    return {b, t, tm, c};
   }
 }
 
@@ -383,7 +392,7 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
           ns_split(acc[i][j][e] * kUpdScale + p.a * (1.f / kLoScale) * rest, h[e], l[e]);
         }
         *place(i, j) = u32x2_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-        lo[(i * F + j) * 64] = u32x2_t{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
+        if (p.keep_lo) lo[(i * F + j) * 64] = u32x2_t{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
       }
     __syncthreads();
     store(p.ynext + b * ysz, p.rp, p.cp, p.rp);
@@ -418,19 +427,22 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
   }
 }
 
-// One W x W tile of a product. 4 waves as 2 x 2; K in stages of 64 through a
-// ring of NS LDS buffers, filled by loads straight to LDS that run NS - 1
-// stages ahead; two workgroups share a CU, so one multiplies while the other
-// waits at its barrier. W = 128 takes 64 KiB of LDS with NS = 2, W = 64 with
-// NS = 4 (its stages are four times shorter, and the loads' latency is not).
+// One W x W tile of a product. 4 waves as 2 x 2; K in stages of 64 (two k-steps)
+// through a ring of NS LDS buffers, filled by loads straight to LDS. A stage's
+// second k-step is multiplied while the next stage's first fragments are read
+// and the loads of stage s + NS are issued into the buffer just released.
+// W = 64, NS = 4 and W = 128, NS = 2 take 64 KiB of LDS, two workgroups per CU;
+// W = 128, NS = 4 is for launches of at most one workgroup per CU, which has
+// nobody to hide its loads' latency. The 128 x 128 tiles are bound by LDS
+// bandwidth (96 KiB per stage, 768 cycles against 512 of MFMA), the 64 x 64
+// ones by their start and end (2500 cycles against 250 to 300 a stage).
 // Each MFMA takes the second operand's fragment first, so a lane ends with
 // four consecutive columns of one row.
-template <int W, int MODE>
-__global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
+template <int W, int NS, int MODE>
+__global__ __launch_bounds__(kNsThreads, W == 128 && NS > 2 ? 1 : 2) void ns_gemm_kernel(NsArgs p) {
   constexpr bool KMAJ = MODE == kGram;
   constexpr bool SYM = MODE == kGram || MODE == kSquare;
   constexpr int OB = W * 128;      // bytes of one operand's stage
-  constexpr int NS = W == 128 ? 2 : 4;
   constexpr int NL = OB / 4096;    // 1 KiB loads per wave, operand and stage
   constexpr int F = W / 32;        // 16-row fragments per wave and operand
   constexpr int NR = KMAJ ? 4 * F : 2 * F;  // LDS reads per wave and k-step
@@ -479,19 +491,23 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
   const char* base_a = reinterpret_cast<const char*>(KMAJ ? opa : opa + (int64_t)row0 * p.rp);
   const char* base_b = reinterpret_cast<const char*>(KMAJ ? opb : opb + (int64_t)col0 * p.rp);
   const int64_t step = KMAJ ? (int64_t)128 * p.rp : 128;  // bytes per stage
-  auto issue = [&](int s) {
+  struct Stage {
+    __amdgpu_buffer_rsrc_t ra, rb;
+    lds_t* d;
+  };
+  auto stage_of = [&](int s) {
     // a stage past the last one gets resources of no records: its loads touch
     // no memory, and the count of loads in flight stays the same
     const int nrec = s < stages ? 0x7ffffff0 : 0;
-    const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base_a + s * step), 0, nrec,
-                                                      kBufFlags);
-    const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base_b + s * step), 0, nrec,
-                                                      kBufFlags);
-    lds_t* d = smem + (s % NS) * 2 * OB + wave * NL * 1024;
-#pragma unroll
-    for (int i = 0; i < NL; ++i) dma16(ra, d + i * 1024, off[0][i]);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) dma16(rb, d + OB + i * 1024, off[1][i]);
+    return Stage{__builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base_a + s * step), 0, nrec,
+                                                   kBufFlags),
+                 __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base_b + s * step), 0, nrec,
+                                                   kBufFlags),
+                 smem + (s % NS) * 2 * OB + wave * NL * 1024};
+  };
+  auto issue = [&](const Stage& s, int i) {
+    if (i < NL) dma16(s.ra, s.d + i * 1024, off[0][i]);
+    else dma16(s.rb, s.d + OB + (i - NL) * 1024, off[1][i - NL]);
   };
 
   f32x4_t acc[F][F];
@@ -543,12 +559,15 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
     else
       return bit_cast<f16x8_t>(f.q[i]);
   };
-  auto multiply = [&](const Frags& fa, const Frags& fb) {
+  auto multiply = [&](const Frags& fa, const Frags& fb, auto&& after) {
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
-      for (int j = 0; j < F; ++j)
+      for (int j = 0; j < F; ++j) {
         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(get(fb, j), get(fa, i), acc[i][j], 0, 0, 0);
+        after(i * F + j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
   };
 
   // What the epilogue reads besides the products, loaded ahead of the main loop
@@ -556,8 +575,12 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
   // the update's lo, the square's tile of A
   constexpr int NE = MODE == kUpdate || MODE == kSquare ? F : 0;
   u32x2_t ext[NE ? NE : 1][NE ? NE : 1];
+  auto fill = [&](int s) {
+    const Stage st = stage_of(s);
 #pragma unroll
-  for (int s = 0; s < NS - 1; ++s) issue(s);
+    for (int i = 0; i < 2 * NL; ++i) issue(st, i);
+  };
+  fill(0);
   if constexpr (MODE == kUpdate) {
     const u32x2_t* lo = ns_lo(p, tl, F);
 #pragma unroll
@@ -576,28 +599,44 @@ __global__ __launch_bounds__(kNsThreads, 2) void ns_gemm_kernel(NsArgs p) {
           ext[i][j] = *reinterpret_cast<const u32x2_t*>(A + (int64_t)r * p.rp + c);
       }
   }
+#pragma unroll
+  for (int s = 1; s < NS; ++s) fill(s);
+  Frags a0, b0, a1, b1;
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 1) * 2 * NL) : "memory");
+  bar_sync();
+  read(b0, s0 + OB, wc, 0);
+  read(a0, s0, wr, 0);
   for (int s = 0; s < stages; ++s) {
-    // this wave's loads of stage s have landed (those of the stages after it
-    // may be in flight: loads complete in order), then every wave's; and every
-    // wave is done with the buffer that the next loads fill
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * 2 * NL) : "memory");
-    bar_sync();
-    const uint32_t sa = s0 + (s % NS) * 2 * OB, sb = sa + OB;
-    Frags a0, b0, a1, b1;
-    read(b0, sb, wc, 0);
-    read(a0, sa, wr, 0);
-    issue(s + NS - 1);
-    read(b1, sb, wc, 1);
+    const uint32_t sa = s0 + (s % NS) * 2 * OB, sn = s0 + ((s + 1) % NS) * 2 * OB;
+    read(b1, sa + OB, wc, 1);
     read(a1, sa, wr, 1);
     lgkm_wait(NR);
     tie(b0);
     tie(a0);
-    multiply(a0, b0);
+    multiply(a0, b0, [](int) {});
+    // every read of this stage is done, by every wave: its buffer may be
+    // filled again; and the next stage has landed (this wave's loads of it,
+    // those of later stages may be in flight: loads complete in order; then
+    // every wave's)
     lgkm_wait(0);
     tie(b1);
     tie(a1);
-    multiply(a1, b1);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * 2 * NL) : "memory");
+    bar_sync();
+    // under the second k-step's products: the next stage's first fragments
+    // (after the last stage: of a buffer nobody fills any more, never used),
+    // and the loads of stage s + NS
+    read(b0, sn + OB, wc, 0);
+    read(a0, sn, wr, 0);
+    const Stage st = stage_of(s + NS);
+    multiply(a1, b1, [&](int q) {
+      constexpr int kEvery = F * F / (2 * NL);
+      if (q % kEvery == kEvery - 1) issue(st, q / kEvery);
+    });
   }
+  lgkm_wait(0);  // the last reads land in registers that stay theirs until then
+  tie(b0);
+  tie(a0);
   wait_vmcnt0();
   __syncthreads();  // every read of the operands is done: their place takes the output
 
@@ -748,32 +787,35 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
   const int r = tall ? n : m, c = tall ? m : n;
   const int64_t gb = (int64_t)blockIdx.x * m * n;
 
+  // element strides of Y's rows and columns in G
+  const int sr = tall ? n : 1, sc = tall ? 1 : n;
   f32x4_t x[RB][CB];
   double sq = 0;
+  // places outside G read its first element, all loads of a row of blocks being
+  // in flight together, and become zeros
+  auto load = [&](auto dtype) {
 #pragma unroll
-  for (int i = 0; i < RB; ++i)
-#pragma unroll
-    for (int j = 0; j < CB; ++j) {
+    for (int i = 0; i < RB; ++i) {
       const int row = (wave * RB + i) * 16 + lr;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int col = j * 16 + lc + e;
-        float v = 0.f;
-        if (row < c && col < r) {
-          const int64_t at = gb + (tall ? (int64_t)row * n + col : (int64_t)col * n + row);
-          if (p.in_dtype == MC2_F32) v = ns_load<MC2_F32>(p.g, at);
-          else if (p.in_dtype == MC2_BF16) v = ns_load<MC2_BF16>(p.g, at);
-          else v = ns_load<MC2_F16>(p.g, at);
+      for (int j = 0; j < CB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = j * 16 + lc + e;
+          const bool in = row < c && col < r;
+          const float v = ns_load<decltype(dtype)::value>(p.g, gb + (in ? row * sr + col * sc : 0));
+          x[i][j][e] = in ? v : 0.f;
         }
-        x[i][j][e] = v;
-      }
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sq = __builtin_fma((double)x[i][j][e], (double)x[i][j][e], sq);
+      __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-  for (int i = 0; i < RB; ++i)
-#pragma unroll
-    for (int j = 0; j < CB; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sq = __builtin_fma((double)x[i][j][e], (double)x[i][j][e], sq);
+  };
+  if (p.in_dtype == MC2_F32) load(std::integral_constant<int, MC2_F32>{});
+  else if (p.in_dtype == MC2_BF16) load(std::integral_constant<int, MC2_BF16>{});
+  else load(std::integral_constant<int, MC2_F16>{});
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) sq += __shfl_xor(sq, off);
   if (lane == 0) s_n[wave] = sq;
@@ -808,7 +850,7 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
     for (int i = 0; i < FA; ++i)
 #pragma unroll
       for (int j = 0; j < FB; ++j) g[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 2
     for (int ks = 0; ks < KS; ++ks) {
       f16x8_t fa[FA], fb[FB];
 #pragma unroll
@@ -889,21 +931,24 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
     // (a wave reads only its own rows of Y above and writes only them in the
     // next step; the reads of Q end before that step's first barrier)
   }
-  const float sc = p.scale / kXScale;
+  const float so = p.scale / kXScale;
+  uint16_t* out = p.out + gb;
+  auto store = [&](auto cvt) {
 #pragma unroll
-  for (int i = 0; i < RB; ++i)
-#pragma unroll
-    for (int j = 0; j < CB; ++j) {
+    for (int i = 0; i < RB; ++i) {
       const int row = (wave * RB + i) * 16 + lr;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int col = j * 16 + lc + e;
-        const float v = x[i][j][e] * sc;
-        if (row < c && col < r)
-          p.out[gb + (tall ? (int64_t)row * n + col : (int64_t)col * n + row)] =
-              p.out_bf16 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v);
-      }
+      for (int j = 0; j < CB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = j * 16 + lc + e;
+          if (row < c && col < r) out[row * sr + col * sc] = cvt(x[i][j][e] * so);
+        }
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  if (p.out_bf16) store([](float v) { return f32_to_bf16_bits(v); });
+  else store([](float v) { return f32_to_f16_bits(v); });
 }
 
 // ---------------------------------------------------------------- host
@@ -960,7 +1005,11 @@ static void ns_start(const void* g, int64_t batch, int64_t m, int64_t n, const N
   else rows16 ? init(ns_init_kernel<D, false, true>) : init(ns_init_kernel<D, false, false>);
 }
 
-// Width of a product's tiles: the widest that gives every CU one.
+// Width of a product's tiles, and p's tile counts for it: 256 where those give
+// every CU a tile (five steps of 16 x 2048 x 1536: 1.78 ms, with 128 at most
+// 2.02 ms), else 128 where those give every second CU one (one 2048 x 3584: 457 us;
+// asking for one on every CU 477 us, and for one on every third, 3 x 777 x 1001
+// goes from 185 to 227 us), else 64.
 template <int MODE>
 static int ns_plan(NsArgs& p, int64_t batch) {
   constexpr bool SYM = MODE == kGram || MODE == kSquare;
@@ -970,17 +1019,27 @@ static int ns_plan(NsArgs& p, int64_t batch) {
     p.tiles_m = (rows + w - 1) / w;
     p.tiles_n = (cols + w - 1) / w;
     p.tiles = SYM ? p.tiles_n * (p.tiles_n + 1) / 2 : p.tiles_m * p.tiles_n;
-    if (w == 64 || batch * p.tiles >= num_cus()) return w;
+    p.row_tiles = SYM ? p.tiles_n + 1 : p.tiles_n;
+    p.inv_tiles = 1.f / static_cast<float>(p.tiles);
+    p.inv_row_tiles = 1.f / static_cast<float>(p.row_tiles);
+    const int64_t n = batch * p.tiles;
+    if (w == 64 || n >= (w == 256 ? num_cus() : num_cus() / 2)) return w;
   }
 }
 
 template <int MODE>
 static void ns_product(NsArgs p, int64_t batch, hipStream_t stream) {
   const int w = ns_plan<MODE>(p, batch);
-  const dim3 grid(static_cast<unsigned>(batch * p.tiles)), blk(kNsThreads);
-  if (w == 256) hipLaunchKernelGGL(ns_gemm256_kernel<MODE>, grid, blk, 0, stream, p);
-  else if (w == 128) hipLaunchKernelGGL((ns_gemm_kernel<128, MODE>), grid, blk, 0, stream, p);
-  else hipLaunchKernelGGL((ns_gemm_kernel<64, MODE>), grid, blk, 0, stream, p);
+  const int64_t n = batch * p.tiles;
+  const dim3 grid(static_cast<unsigned>(n)), blk(kNsThreads);
+  if (w == 256)
+    hipLaunchKernelGGL(ns_gemm256_kernel<MODE>, grid, blk, 0, stream, p);
+  else if (w == 128 && n <= num_cus())
+    hipLaunchKernelGGL((ns_gemm_kernel<128, 4, MODE>), grid, blk, 0, stream, p);
+  else if (w == 128)
+    hipLaunchKernelGGL((ns_gemm_kernel<128, 2, MODE>), grid, blk, 0, stream, p);
+  else
+    hipLaunchKernelGGL((ns_gemm_kernel<64, 4, MODE>), grid, blk, 0, stream, p);
 }
 
 // The whole call as one launch, for matrices that one workgroup can hold.
@@ -1027,8 +1086,8 @@ extern "C" int mc2_ns_orthogonalize(const void* g, int64_t batch, int64_t m, int
     if (!(coeffs[i] >= -16.f && coeffs[i] <= 16.f)) return MC2_ERR_SHAPE;
   if (!aligned16(g) || !aligned16(out) || !aligned16(workspace)) return MC2_ERR_ALIGN;
   const NsLayout L = ns_layout(batch, m, n);
-  // grids are 32-bit: tiles of 64 x 64 of the largest product
-  if (batch * (L.cp / 64) * (L.cp / 64) > 0x7fffffff) return MC2_ERR_SHAPE;
+  // tiles of 64 x 64 of the largest product (ns_div; 128 GiB of iterate)
+  if (batch * (L.cp / 64) * (L.rp / 64) >= 1 << 24) return MC2_ERR_SHAPE;
   if (ws_bytes < L.total) return MC2_ERR_WORKSPACE;
   TinyArgs ta{};
   ta.g = g;
@@ -1068,6 +1127,7 @@ extern "C" int mc2_ns_orthogonalize(const void* g, int64_t batch, int64_t m, int
     p.a = coeffs[3 * s];
     p.b = coeffs[3 * s + 1];
     p.c = coeffs[3 * s + 2];
+    p.keep_lo = s + 2 < steps;  // the last step reads hi only
     ns_product<kGram>(p, batch, stream);
     ns_product<kSquare>(p, batch, stream);
     if (!last) ns_product<kUpdate>(p, batch, stream);
