@@ -723,7 +723,8 @@ __global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
 // wave w owns 16-row blocks w * RB .. + RB - 1 and holds their values in fp32 in
 // registers, in the accumulator layout: the product Y Q is added onto a Y held
 // there, so no low half is needed, and a wave's update touches its own rows
-// only. A and Q take turns in one (rp, rp) LDS array.
+// only. A (less mu I) and Q take turns in one (rp, rp) LDS array. 64 x 256 takes
+// 11 us of GPU time, 64 x 1000 and 128 x 512 40 and 60 us.
 constexpr int kTinyThreads = 512;
 constexpr int64_t kTinyElems = 65536;
 
@@ -837,7 +838,12 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
 
   const int wm = (wave >> 1) * (RP / 4), wn = (wave & 1) * (RP / 2);  // this wave's part of A, Q
   for (int s = 0; s < p.steps; ++s) {
-    const float a = p.co[3 * s], b = p.co[3 * s + 1], cc = p.co[3 * s + 2];
+    // A is held as D = A - mu I, whose diagonal is smaller than A's once the
+    // singular values are near 1 (there most of the rounding of A A comes from):
+    // a I + b A + c A A = (a + b mu + c mu^2) I + (b + 2 c mu) D + c D D
+    const float mu = s < 2 ? 0.f : 0.5f;
+    const float cc = p.co[3 * s + 2], b = p.co[3 * s + 1] + 2.f * cc * mu;
+    const float a = p.co[3 * s], am = (p.co[3 * s + 1] + cc * mu) * mu;
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
@@ -868,7 +874,9 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
 #pragma unroll
       for (int j = 0; j < FB; ++j) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) g[i][j][e] *= kGramScale;
+        for (int e = 0; e < 4; ++e)
+          g[i][j][e] = g[i][j][e] * kGramScale -
+                       (wm + i * 16 + lr == wn + j * 16 + lc + e ? mu * kDiag : 0.f);
         tiny_put<RP>(s_a, wm + i * 16 + lr, wn + j * 16 + lc, g[i][j][0], g[i][j][1], g[i][j][2],
                      g[i][j][3]);
       }
@@ -902,14 +910,23 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
                      q[i][j][3]);
       }
     __syncthreads();
-    // x = a x + Y Q: the product's scale is 2^21, x's 2^12
+    // x = a x + (b mu + c mu^2) hi + hi Q: the part of the identity that the
+    // product takes away again is added to what the product multiplies, hi (its
+    // rounding would else stay in the directions of singular value zero).
+    // The product's scale is 2^21, x's 2^12.
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-      for (int j = 0; j < CB; ++j)
+      for (int j = 0; j < CB; ++j) {
+        // (opaque: hi is formed anew here, not kept in registers from the step's
+        // start)
+        asm volatile("" : "+v"(x[i][j]));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][j][e] *= a * (1.f / kUpdScale);
-#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[i][j][e] = (a * x[i][j][e] + am * f16_bits_to_f32(f32_to_f16_bits(x[i][j][e]))) *
+                       (1.f / kUpdScale);
+      }
+#pragma unroll 1
     for (int ks = 0; ks < RP / 32; ++ks) {
       f16x8_t fa[RB];
 #pragma unroll
