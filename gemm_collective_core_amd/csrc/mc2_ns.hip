@@ -777,6 +777,7 @@ __device__ __forceinline__ void tiny_put(char* s, int r, int c, float a, float b
 template <int RP, int RB>
 __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
   constexpr int CB = RP / 16, KS = RB * 4;  // 32-row k steps of Y
+  constexpr int kGramUnroll = RP == 64 && RB <= 4 ? 4 : 2;  // (registers)
   constexpr int FA = RP / 64, FB = RP / 32;  // a wave's 16-row / 16-column blocks of A and Q
   __shared__ __attribute__((aligned(16))) char s_y[RB * 128 * RP * 2];
   __shared__ __attribute__((aligned(16))) char s_a[RP * RP * 2];
@@ -825,16 +826,22 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
 #pragma unroll
   for (int w = 0; w < kTinyThreads / 64; ++w) norm2 += s_n[w];
   const double inv = norm2 == 0.0 ? 0.0 : kXScale / (sqrt(norm2) + static_cast<double>(p.eps));
+  const float invf = static_cast<float>(inv);
+  // in fp64 only where fp32 does not hold 1 / norm (what lies outside G stays
+  // zero: inv may be NaN)
+  auto normalise = [&](auto mul) {
 #pragma unroll
-  for (int i = 0; i < RB; ++i)
+    for (int i = 0; i < RB; ++i)
 #pragma unroll
-    for (int j = 0; j < CB; ++j) {
-      const int row = (wave * RB + i) * 16 + lr;
+      for (int j = 0; j < CB; ++j) {
+        const int row = (wave * RB + i) * 16 + lr;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)  // (what lies outside G stays zero: inv may be NaN)
-        if (row < c && j * 16 + lc + e < r)
-          x[i][j][e] = static_cast<float>(static_cast<double>(x[i][j][e]) * inv);
-    }
+        for (int e = 0; e < 4; ++e)
+          x[i][j][e] = row < c && j * 16 + lc + e < r ? mul(x[i][j][e]) : 0.f;
+      }
+  };
+  if (invf > 1e-30f && invf < 1e30f) normalise([&](float v) { return v * invf; });
+  else normalise([&](float v) { return static_cast<float>(static_cast<double>(v) * inv); });
 
   const int wm = (wave >> 1) * (RP / 4), wn = (wave & 1) * (RP / 2);  // this wave's part of A, Q
   for (int s = 0; s < p.steps; ++s) {
@@ -856,7 +863,7 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
     for (int i = 0; i < FA; ++i)
 #pragma unroll
       for (int j = 0; j < FB; ++j) g[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
+#pragma unroll kGramUnroll
     for (int ks = 0; ks < KS; ++ks) {
       f16x8_t fa[FA], fb[FB];
 #pragma unroll
@@ -948,24 +955,51 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
     // (a wave reads only its own rows of Y above and writes only them in the
     // next step; the reads of Q end before that step's first barrier)
   }
+  // The result takes Y's place (a wave's rows are read by that wave alone once Q
+  // is formed) and leaves in 16-byte pieces of G's rows where those are whole
+  // (2-byte stores from the registers took 18 us for 128 x 512).
   const float so = p.scale / kXScale;
+  auto stage = [&](auto cvt) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < CB; ++j) {
+        const int row = (wave * RB + i) * 16 + lr, col = j * 16 + lc;
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = cvt(x[i][j][e] * so);
+        *reinterpret_cast<u32x2_t*>(s_y + tiny_pos<RP>(row, col >> 3) + ((col & 4) << 1)) =
+            u32x2_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+      }
+  };
+  if (p.out_bf16) stage([](float v) { return f32_to_bf16_bits(v); });
+  else stage([](float v) { return f32_to_f16_bits(v); });
+  __syncthreads();
   uint16_t* out = p.out + gb;
-  auto store = [&](auto cvt) {
+  // eight values of one row of G, from column `at` on
+  auto put8 = [&](u32x4_t v, int row, int at) {
+    if (n % 8 == 0) {
+      *reinterpret_cast<u32x4_t*>(out + row * n + at) = v;
+    } else {
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      const int row = (wave * RB + i) * 16 + lr;
-#pragma unroll
-      for (int j = 0; j < CB; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = j * 16 + lc + e;
-          if (row < c && col < r) out[row * sr + col * sc] = cvt(x[i][j][e] * so);
-        }
-      __builtin_amdgcn_sched_barrier(0);
+      for (int e = 0; e < 8; ++e)
+        if (at + e < n) out[row * n + at + e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
     }
   };
-  if (p.out_bf16) store([](float v) { return f32_to_bf16_bits(v); });
-  else store([](float v) { return f32_to_f16_bits(v); });
+  if (tall) {
+    for (int q = tid; q < c * (RP / 8); q += kTinyThreads) {
+      const int row = q / (RP / 8), ch = q % (RP / 8);
+      if (ch * 8 < r)
+        put8(*reinterpret_cast<const u32x4_t*>(s_y + tiny_pos<RP>(row, ch)), row, ch * 8);
+    }
+  } else {
+    for (int q = wave; q < KS * CB; q += kTinyThreads / 64) {
+      const int c0 = (q / KS) * 16, ks = q % KS;
+      const u32x4_t v = bit_cast<u32x4_t>(tiny_col<RP>(s_y, c0, ks));
+      const int col = c0 + lr, row = ks * 32 + (lane >> 4) * 8;
+      if (col < r && row < c) put8(v, col, row);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- host
