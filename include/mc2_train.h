@@ -88,14 +88,16 @@ int mc2_moe_permute_backward(const void* dpermuted, int64_t rows, const int32_t*
  *     mc2_ns_workspace_size(batch, m, n) bytes, no initialisation needed.
  *     Calls that overlap in time must not share one.
  * Constraints: 1 <= batch <= 65535, 1 <= m, n <= 65536 (any sizes: rows need
- * not be whole 16-byte pieces). mc2_ns_workspace_size gives 0 for sizes outside.
+ * not be whole 16-byte pieces); mc2_ns_workspace_size gives 0 for sizes outside.
+ * batch * ceil(m / 64) * ceil(n / 64) < 2^24 (128 GiB for one copy of the
+ * iterate), else MC2_ERR_SHAPE.
  *
  * Precision: the norm is summed in fp64. Products take operands rounded to
- * fp16 (scaled by powers of two) and accumulate in fp32; the iterate is held to
- * 22 bits in the term a X, so that rounding noise in directions whose singular
- * value is near zero is not multiplied by a in every step. The result is
- * within about 2e-3 (2-norm of the difference over that of the result) before
- * its rounding to out_dtype with the usual five steps of
+ * fp16 (scaled by powers of two) and accumulate in fp32; the iterate itself is
+ * held to 22 bits or more until the last step, so that rounding noise in
+ * directions whose singular value is near zero is not multiplied by a in every
+ * step. The result is within 1e-3 to 2.5e-3 (2-norm of the difference over that
+ * of the result) before its rounding to out_dtype with the usual five steps of
  * (3.4445, -4.7750, 2.0315), whatever the rank of G. Iterates are held in
  * range as long as their entries stay below 16 and the entries of A and
  * b A + c A A below 128 (coefficients whose iterates stay bounded, as those

@@ -71,8 +71,11 @@ def test_rank_deficient(m, n, rank):
     _check(g, mc2.mc2_ns_orthogonalize(g.cuda()))
 
 
-def test_a_matrix_of_the_stack_does_not_see_the_others():
-    g = torch.randn((4, 96, 160), generator=torch.Generator().manual_seed(1)).cuda()
+@pytest.mark.parametrize("m,n", [(96, 160), (200, 160), (260, 513)])
+def test_a_matrix_of_the_stack_does_not_see_the_others(m, n):
+    """Zeros, NaN and infinities beside an ordinary matrix, which gets the bits
+    it gets alone."""
+    g = torch.randn((4, m, n), generator=torch.Generator().manual_seed(1)).cuda()
     alone = mc2.mc2_ns_orthogonalize(g[1:2].contiguous(), eps=0.0)
     g[0] = 0
     g[2, 5, 7] = float("nan")
@@ -84,15 +87,17 @@ def test_a_matrix_of_the_stack_does_not_see_the_others():
     assert torch.isnan(o[2]).all() and torch.isnan(o[3]).all()
 
 
-@pytest.mark.parametrize("mag", [1e-30, 1e-12, 1e12, 1e30])
-def test_magnitudes(mag):
+@pytest.mark.parametrize("m,n", [(100, 140), (200, 140)])
+@pytest.mark.parametrize("mag", [1e-36, 1e-30, 1e-12, 1e12, 1e30, 1e36])
+def test_magnitudes(mag, m, n):
     """The norm neither vanishes nor overflows."""
-    g = torch.randn((100, 140), generator=torch.Generator().manual_seed(2)) * mag
+    g = torch.randn((m, n), generator=torch.Generator().manual_seed(2)) * mag
     _check(g, mc2.mc2_ns_orthogonalize(g.cuda(), eps=0.0), eps=0.0)
 
 
-def test_steps_coefficients_eps_scale_and_2d():
-    g = torch.randn((90, 150), generator=torch.Generator().manual_seed(3))
+@pytest.mark.parametrize("m,n", [(90, 150), (150, 200)])
+def test_steps_coefficients_eps_scale_and_2d(m, n):
+    g = torch.randn((m, n), generator=torch.Generator().manual_seed(3))
     gd = g.cuda()
     for steps in (1, 2, 3):
         _check(g, mc2.mc2_ns_orthogonalize(gd, steps=steps), coeffs=(CO,) * steps)
@@ -129,3 +134,25 @@ def test_given_buffers_streams_and_repeats():
     inplace = gs[0].clone()
     mc2.mc2_ns_orthogonalize(inplace, out=inplace)
     assert torch.equal(inplace.view(torch.int16), ref[0].view(torch.int16))
+
+
+@pytest.mark.parametrize("B,m,n", [(2, 50, 120), (3, 200, 304), (90, 264, 520)])
+def test_captured_and_replayed(B, m, n):
+    """Replays of one captured call, with new values, eager calls on the same
+    workspace and synchronizations between them, give the eager bits."""
+    gen = torch.Generator().manual_seed(5)
+    gs = [torch.randn((B, m, n), generator=gen).cuda() for _ in range(2)]
+    ws = torch.empty(mc2.mc2_ns_workspace_size(B, m, n), dtype=torch.uint8, device="cuda")
+    eager = [mc2.mc2_ns_orthogonalize(g, workspace=ws) for g in gs]
+    g, o = gs[0].clone(), torch.empty_like(eager[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mc2.mc2_ns_orthogonalize(g, out=o, workspace=ws)
+    for i in (1, 0, 0, 1):
+        g.copy_(gs[i])
+        o.fill_(3.0)
+        mc2.mc2_ns_orthogonalize(gs[1 - i], workspace=ws)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o.view(torch.int16), eager[i].view(torch.int16)), i
