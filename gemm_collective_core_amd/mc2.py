@@ -518,6 +518,15 @@ def mc2_moe_unpermute(y_full, unpermute_idx, probs, *, out=None, dev_err=None):
     return out
 
 
+def _call(dev, fn, *args):
+    """fn(*args) with dev as the current device (entering it costs more than a
+    small launch, so only where it is another one)."""
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def mc2_moe_unpermute_backward(dout, y_full, unpermute_idx, sorted_idx, probs, *, dy=None,
                                dprobs=None, need_dy=True, need_dprobs=True, dev_err=None):
     """Gradient of mc2_moe_unpermute: returns (dy, dprobs), None in the place
@@ -544,11 +553,10 @@ def mc2_moe_unpermute_backward(dout, y_full, unpermute_idx, sorted_idx, probs, *
     if need_dprobs and dprobs is None:
         dprobs = torch.empty((T, K), dtype=torch.float32, device=dev)
     dprobs = dprobs if need_dprobs else None
-    with torch.cuda.device(dev):
-        st = _lib.load().mc2_moe_unpermute_backward(
-            dout.data_ptr(), y_full.data_ptr(), y_full.shape[0], unpermute_idx.data_ptr(),
-            sorted_idx.data_ptr(), probs.data_ptr(), T, K, H, _CODES[dout.dtype], _ptr(dy),
-            _ptr(dprobs), _ptr(dev_err), _stream(dev))
+    st = _call(dev, _lib.load().mc2_moe_unpermute_backward, dout.data_ptr(), y_full.data_ptr(),
+               y_full.shape[0], unpermute_idx.data_ptr(), sorted_idx.data_ptr(),
+               probs.data_ptr(), T, K, H, _CODES[dout.dtype], _ptr(dy), _ptr(dprobs),
+               _ptr(dev_err), _stream(dev))
     _check("mc2_moe_unpermute_backward", st)
     return dy, dprobs
 
@@ -568,10 +576,9 @@ def mc2_moe_permute_backward(dpermuted, unpermute_idx, topk, *, dx=None, dev_err
     dev = _dev(dpermuted, unpermute_idx, dx, dev_err)
     if dx is None:
         dx = torch.empty((T, H), dtype=dpermuted.dtype, device=dev)
-    with torch.cuda.device(dev):
-        st = _lib.load().mc2_moe_permute_backward(
-            dpermuted.data_ptr(), dpermuted.shape[0], unpermute_idx.data_ptr(), T, topk, H,
-            _CODES[dpermuted.dtype], dx.data_ptr(), _ptr(dev_err), _stream(dev))
+    st = _call(dev, _lib.load().mc2_moe_permute_backward, dpermuted.data_ptr(),
+               dpermuted.shape[0], unpermute_idx.data_ptr(), T, topk, H,
+               _CODES[dpermuted.dtype], dx.data_ptr(), _ptr(dev_err), _stream(dev))
     _check("mc2_moe_permute_backward", st)
     return dx
 
@@ -607,10 +614,8 @@ def mc2_ns_orthogonalize(g, *, steps=5, coeffs=MC2_NS_COEFFS, eps=1e-7, scale=1.
     if out is None:
         out = torch.empty(g.shape, dtype=out_dtype, device=dev)
     workspace = _workspace(mc2_ns_workspace_size(batch, m, n), workspace, dev)
-    with torch.cuda.device(dev):
-        st = _lib.load().mc2_ns_orthogonalize(
-            g.data_ptr(), batch, m, n, _CODES[g.dtype], steps,
-            (ctypes.c_float * len(flat))(*flat), eps, scale, _CODES[out_dtype], out.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), _stream(dev))
+    st = _call(dev, _lib.load().mc2_ns_orthogonalize, g.data_ptr(), batch, m, n, _CODES[g.dtype],
+               steps, (ctypes.c_float * len(flat))(*flat), eps, scale, _CODES[out_dtype],
+               out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(dev))
     _check("mc2_ns_orthogonalize", st)
     return out
