@@ -46,24 +46,41 @@ __device__ __forceinline__ float ns_load(const void* p, int64_t i) {
   else return f16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
 
-// Eight consecutive values from a 16-byte aligned place.
+// 16 bytes at any element's address (rows of odd length start anywhere; such an
+// access is one load or store here, not split)
+typedef f32x4_t __attribute__((aligned(4))) f32x4_any_t;
+typedef u32x4_t __attribute__((aligned(2))) u32x4_any_t;
+
+// Eight consecutive values.
 template <int D>
 __device__ __forceinline__ void ns_load8(const void* p, int64_t i, float (&v)[8]) {
   if constexpr (D == MC2_F32) {
-    const f32x4_t* q = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + i);
-    const f32x4_t a = q[0], b = q[1];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = a[j];
-      v[4 + j] = b[j];
+    for (int h = 0; h < 2; ++h) {
+      const f32x4_t a = *reinterpret_cast<const f32x4_any_t*>(static_cast<const float*>(p) + i + 4 * h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * h + j] = a[j];
     }
   } else {
-    const u32x4_t q = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + i);
+    const u32x4_t q = *reinterpret_cast<const u32x4_any_t*>(static_cast<const uint16_t*>(p) + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[2 * j] = D == MC2_BF16 ? bf16_bits_to_f32(q[j] & 0xFFFFu) : f16_bits_to_f32(q[j] & 0xFFFFu);
       v[2 * j + 1] = D == MC2_BF16 ? bf16_bits_to_f32(q[j] >> 16) : f16_bits_to_f32(q[j] >> 16);
     }
+  }
+}
+// The same from row `row`, column `col` of a matrix of m rows of n values:
+// zeros outside.
+template <int D>
+__device__ __forceinline__ void ns_load_in(const void* g, int64_t base, int64_t m, int64_t n,
+                                           int64_t row, int64_t col, float (&v)[8]) {
+  if (row < m && col + 8 <= n) {
+    ns_load8<D>(g, base + row * n + col, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = row < m && col + j < n ? ns_load<D>(g, base + row * n + col + j) : 0.f;
   }
 }
 
@@ -81,27 +98,24 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 // part[b][i]: sums of squares, in double (gradients of 1e-30 or 1e30 neither
-// vanish nor overflow).
-template <int D, bool VEC>
+// vanish nor overflow). 16 values per thread in flight.
+template <int D>
 __global__ __launch_bounds__(kNsThreads) void ns_norm_kernel(const void* __restrict__ g, int64_t mn,
                                                              double* __restrict__ part) {
   const int nb = gridDim.x, b = blockIdx.y;
   const int64_t base = (int64_t)b * mn;
+  const int64_t t = (int64_t)blockIdx.x * kNsThreads + threadIdx.x, step = (int64_t)nb * kNsThreads * 8;
   double s = 0;
-  if constexpr (VEC) {
-    for (int64_t i = ((int64_t)blockIdx.x * kNsThreads + threadIdx.x) * 8; i < mn;
-         i += (int64_t)nb * kNsThreads * 8) {
-      float v[8];
-      ns_load8<D>(g, base + i, v);
+  for (int64_t i = t * 8; i < mn; i += 2 * step) {
+    float v[2][8];
+    const bool two = i + step < mn;
+    ns_load_in<D>(g, base, 1, mn, 0, i, v[0]);
+    if (two) ns_load_in<D>(g, base, 1, mn, 0, i + step, v[1]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s = __builtin_fma((double)v[j], (double)v[j], s);
-    }
-  } else {
-    for (int64_t i = (int64_t)blockIdx.x * kNsThreads + threadIdx.x; i < mn;
-         i += (int64_t)nb * kNsThreads) {
-      const double v = ns_load<D>(g, base + i);
-      s = __builtin_fma(v, v, s);
-    }
+    for (int j = 0; j < 8; ++j) s = __builtin_fma((double)v[0][j], (double)v[0][j], s);
+    if (two)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = __builtin_fma((double)v[1][j], (double)v[1][j], s);
   }
   s = block_sum(s);
   if (threadIdx.x == 0) part[(int64_t)b * nb + blockIdx.x] = s;
@@ -127,53 +141,57 @@ __device__ __forceinline__ int64_t ns_lo_place(int row, int col, int w, int tile
 }
 
 // One 64 x 64 tile of Y = G / (|G| + eps), transposed for a wide G, with zeros
-// beyond G. VEC: G's rows are whole 16-byte pieces.
-template <int D, bool TALL, bool VEC>
+// beyond G: read in whole pieces of G's rows into LDS, then hi written in whole
+// 128-byte lines and lo in the update's lane order. Bound by HBM (16 x 2048 x
+// 1536: 403 MB).
+template <int D, bool TALL>
 __global__ __launch_bounds__(kNsThreads) void ns_init_kernel(
     const void* __restrict__ g, int64_t m, int64_t n, const double* __restrict__ part, int nb,
     float eps, int64_t cp, int64_t rp, uint16_t* __restrict__ yhi, u32x2_t* __restrict__ ylo,
     int64_t lo_size, int w, int tiles_n) {
   __shared__ float s_t[64][65];
   const int b = blockIdx.y, tid = threadIdx.x;
-  const double norm2 = block_sum(tid < nb ? part[(int64_t)b * nb + tid] : 0.0);
-  // a matrix of zeros stays one, also with eps = 0
-  const double inv = norm2 == 0.0 ? 0.0 : kXScale / (sqrt(norm2) + static_cast<double>(eps));
   const int tc = static_cast<int>(rp / 64);
   const int64_t y0 = (int64_t)(blockIdx.x / tc) * 64, x0 = (int64_t)(blockIdx.x % tc) * 64;
-  const int64_t gb = (int64_t)b * m * n;
-  // G's tile: rows gr0 .., columns gc0 ..
-  const int64_t gr0 = TALL ? y0 : x0, gc0 = TALL ? x0 : y0;
-  for (int i = tid; i < 64 * 8; i += kNsThreads) {
-    const int r = i >> 3, c8 = (i & 7) * 8;
-    float v[8];
-    const bool row_in = gr0 + r < m;
-    if (VEC && row_in && gc0 + c8 < n) {
-      ns_load8<D>(g, gb + (gr0 + r) * n + gc0 + c8, v);
-    } else {
+  const int64_t gr0 = TALL ? y0 : x0, gc0 = TALL ? x0 : y0;  // the tile in G
+  float u[2][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = row_in && gc0 + c8 + j < n ? ns_load<D>(g, gb + (gr0 + r) * n + gc0 + c8 + j) : 0.f;
-    }
+  for (int h = 0; h < 2; ++h) {
+    const int i = tid + h * kNsThreads;
+    ns_load_in<D>(g, (int64_t)b * m * n, m, n, gr0 + (i >> 3), gc0 + (i & 7) * 8, u[h]);
+  }
+  const double norm2 = block_sum(tid < nb ? part[(int64_t)b * nb + tid] : 0.0);
+  // a matrix of zeros stays one, also with eps = 0; in fp64 where fp32 does not
+  // hold 1 / norm
+  const double inv = norm2 == 0.0 ? 0.0 : kXScale / (sqrt(norm2) + static_cast<double>(eps));
+  const float invf = static_cast<float>(inv);
+  const bool fits = invf > 1e-30f && invf < 1e30f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = tid + h * kNsThreads, r = i >> 3, c = (i & 7) * 8;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const bool in = row_in && gc0 + c8 + j < n;
-      s_t[r][c8 + j] = in ? static_cast<float>(static_cast<double>(v[j]) * inv) : 0.f;
+      const float x = fits ? u[h][j] * invf : static_cast<float>(static_cast<double>(u[h][j]) * inv);
+      // (inv may be NaN: what lies beyond G stays zero)
+      s_t[r][c + j] = gr0 + r < m && gc0 + c + j < n ? x : 0.f;
     }
   }
   __syncthreads();
   auto at = [&](int r, int c) { return TALL ? s_t[r][c] : s_t[c][r]; };
-  for (int i = tid; i < 64 * 8; i += kNsThreads) {
-    const int r = i >> 3, c8 = (i & 7) * 8;
-    u32x4_t h;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = tid + h * kNsThreads, r = i >> 3, c = (i & 7) * 8;
+    u32x4_t v;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      h[j] = f32_to_f16_bits(at(r, c8 + 2 * j)) |
-             (static_cast<uint32_t>(f32_to_f16_bits(at(r, c8 + 2 * j + 1))) << 16);
-    *reinterpret_cast<u32x4_t*>(yhi + (int64_t)b * cp * rp + (y0 + r) * rp + x0 + c8) = h;
+      v[j] = f32_to_f16_bits(at(r, c + 2 * j)) |
+             (static_cast<uint32_t>(f32_to_f16_bits(at(r, c + 2 * j + 1))) << 16);
+    *reinterpret_cast<u32x4_t*>(yhi + (int64_t)b * cp * rp + (y0 + r) * rp + x0 + c) = v;
   }
-  // lo: a wave takes one 16 x 16 block at a time, its lanes as the update's
-  for (int i = tid; i < 64 * 16; i += kNsThreads) {
-    const int blk = i >> 6, l = i & 63;
+  // a wave takes one 16 x 16 block at a time, its lanes as the update's
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int blk = (tid >> 6) * 4 + k, l = tid & 63;
     const int r = (blk >> 2) * 16 + (l & 15), c = (blk & 3) * 16 + (l >> 4) * 4;
     uint32_t h, q[4];
 #pragma unroll
@@ -262,6 +280,17 @@ __device__ __forceinline__ int ns_kswz(int kr) {
 __device__ __forceinline__ u32x2_t* ns_lo(const NsArgs& p, const NsTile& tl, int f) {
   return p.ylo + tl.b * p.lo_size + (int64_t)(tl.t * 4 + (threadIdx.x >> 6)) * (f * f * 64) +
          (threadIdx.x & 63);
+}
+
+// Eight 16-bit values to columns c .. of a row of n.
+__device__ __forceinline__ void ns_put8(uint16_t* row, int c, int n, u32x4_t v) {
+  if (c + 8 <= n) {
+    *reinterpret_cast<u32x4_any_t*>(row + c) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < n) row[c + e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+  }
 }
 
 // Place of 16-byte chunk c of row r of a W x W tile of 16-bit values staged in
@@ -417,11 +446,10 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
     if (p.on % 8 == 0) {
       store(out, p.on, p.om, p.on);
     } else {  // rows that are not whole 16-byte pieces
-      for (int q = tid; q < W * W; q += kNsThreads) {
-        const int r = q / W, c = q - r * W;
-        if (row0 + r < p.om && col0 + c < p.on)
-          out[(int64_t)(row0 + r) * p.on + col0 + c] = *reinterpret_cast<const MC2_LDS uint16_t*>(
-              smem + ns_spos<W>(r, c >> 3) + (c & 7) * 2);
+      for (int q = tid; q < W * (W / 8); q += kNsThreads) {
+        const int r = q / (W / 8), c8 = (q % (W / 8)) * 8;
+        const u32x4_t v = *reinterpret_cast<const MC2_LDS u32x4_t*>(smem + ns_spos<W>(r, c8 >> 3));
+        if (row0 + r < p.om) ns_put8(out + (int64_t)(row0 + r) * p.on, col0 + c8, p.on, v);
       }
     }
   }
@@ -956,8 +984,7 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
     // next step; the reads of Q end before that step's first barrier)
   }
   // The result takes Y's place (a wave's rows are read by that wave alone once Q
-  // is formed) and leaves in 16-byte pieces of G's rows where those are whole
-  // (2-byte stores from the registers took 18 us for 128 x 512).
+  // is formed) and leaves in 16-byte pieces of G's rows (2-byte stores from the registers took 18 us for 128 x 512).
   const float so = p.scale / kXScale;
   auto stage = [&](auto cvt) {
 #pragma unroll
@@ -976,28 +1003,19 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
   else stage([](float v) { return f32_to_f16_bits(v); });
   __syncthreads();
   uint16_t* out = p.out + gb;
-  // eight values of one row of G, from column `at` on
-  auto put8 = [&](u32x4_t v, int row, int at) {
-    if (n % 8 == 0) {
-      *reinterpret_cast<u32x4_t*>(out + row * n + at) = v;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at + e < n) out[row * n + at + e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
-    }
-  };
   if (tall) {
     for (int q = tid; q < c * (RP / 8); q += kTinyThreads) {
       const int row = q / (RP / 8), ch = q % (RP / 8);
       if (ch * 8 < r)
-        put8(*reinterpret_cast<const u32x4_t*>(s_y + tiny_pos<RP>(row, ch)), row, ch * 8);
+        ns_put8(out + row * n, ch * 8, n,
+                *reinterpret_cast<const u32x4_t*>(s_y + tiny_pos<RP>(row, ch)));
     }
   } else {
     for (int q = wave; q < KS * CB; q += kTinyThreads / 64) {
       const int c0 = (q / KS) * 16, ks = q % KS;
       const u32x4_t v = bit_cast<u32x4_t>(tiny_col<RP>(s_y, c0, ks));
       const int col = c0 + lr, row = ks * 32 + (lane >> 4) * 8;
-      if (col < r && row < c) put8(v, col, row);
+      if (col < r && row < c) ns_put8(out + col * n, row, n, v);
     }
   }
 }
@@ -1038,22 +1056,19 @@ static void ns_start(const void* g, int64_t batch, int64_t m, int64_t n, const N
                      float eps, double* part, uint16_t* y, const NsArgs& p, int w,
                      hipStream_t stream) {
   const int64_t mn = m * n;
-  constexpr int per16 = D == MC2_F32 ? 4 : 8;
-  int64_t nb = (mn + kNsThreads * 32 - 1) / (kNsThreads * 32);
+  int64_t nb = (mn + kNsThreads * 16 - 1) / (kNsThreads * 16);
   nb = nb < kNsMaxPart ? nb : kNsMaxPart;
-  const dim3 gn(static_cast<unsigned>(nb), static_cast<unsigned>(batch)), blk(kNsThreads);
-  const bool flat = mn % 8 == 0;  // every matrix starts on 16 bytes and is whole pieces
-  if (flat) hipLaunchKernelGGL((ns_norm_kernel<D, true>), gn, blk, 0, stream, g, mn, part);
-  else hipLaunchKernelGGL((ns_norm_kernel<D, false>), gn, blk, 0, stream, g, mn, part);
-  const dim3 gi(static_cast<unsigned>(L.cp / 64 * (L.rp / 64)), static_cast<unsigned>(batch));
-  const bool rows16 = n % 8 == 0;
-  static_assert(per16 == 4 || per16 == 8, "16-byte pieces");
+  const dim3 blk(kNsThreads);
+  hipLaunchKernelGGL(ns_norm_kernel<D>, dim3(static_cast<unsigned>(nb), static_cast<unsigned>(batch)),
+                     blk, 0, stream, g, mn, part);
   auto init = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, gi, blk, 0, stream, g, m, n, part, static_cast<int>(nb), eps, L.cp,
-                       L.rp, y, p.ylo, p.lo_size, w, static_cast<int>((L.rp + w - 1) / w));
+    hipLaunchKernelGGL(kernel,
+                       dim3(static_cast<unsigned>(L.cp / 64 * (L.rp / 64)), static_cast<unsigned>(batch)),
+                       blk, 0, stream, g, m, n, part, static_cast<int>(nb), eps, L.cp, L.rp, y, p.ylo,
+                       p.lo_size, w, static_cast<int>((L.rp + w - 1) / w));
   };
-  if (m >= n) rows16 ? init(ns_init_kernel<D, true, true>) : init(ns_init_kernel<D, true, false>);
-  else rows16 ? init(ns_init_kernel<D, false, true>) : init(ns_init_kernel<D, false, false>);
+  if (m >= n) init(ns_init_kernel<D, true>);
+  else init(ns_init_kernel<D, false>);
 }
 
 // Width of a product's tiles, and p's tile counts for it: 256 where those give
