@@ -306,9 +306,8 @@ __device__ __forceinline__ int ns_spos(int r, int c) {
 // Everything after the products of a W x W tile, held as F x F blocks of
 // accumulators per wave (2 x 2 waves; a lane has four consecutive columns of
 // one row), staged through `smem` for whole-row stores. ext(i, j): the block's
-// four values of lo (update) or, with !A_IN_LDS, of A (square), asked for in
-// order; with A_IN_LDS A's tile lies in `smem` and Q~ takes its place.
-template <int W, int MODE, int F, bool A_IN_LDS, class Ext>
+// four values of lo (update) or of A (square), asked for in order.
+template <int W, int MODE, int F, class Ext>
 __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, lds_t* smem,
                                             const f32x4_t (&acc)[F][F], Ext&& ext) {
   constexpr bool SYM = MODE == kGram || MODE == kSquare;
@@ -363,9 +362,7 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
         } else {
           const int r = row0 + wr + i * 16 + (lane & 15);
           const int c = col0 + wc + j * 16 + 4 * (lane >> 4);
-          u32x2_t x;
-          if constexpr (A_IN_LDS) x = *place(i, j);
-          else x = ext(i, j);
+          const u32x2_t x = ext(i, j);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float g = f16_bits_to_f32((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
@@ -668,7 +665,7 @@ __global__ __launch_bounds__(kNsThreads, W == 128 && NS > 2 ? 1 : 2) void ns_gem
   wait_vmcnt0();
   __syncthreads();  // every read of the operands is done: their place takes the output
 
-  ns_epilogue<W, MODE, F, false>(p, tl, smem, acc, [&](int i, int j) { return ext[NE ? i : 0][NE ? j : 0]; });
+  ns_epilogue<W, MODE, F>(p, tl, smem, acc, [&](int i, int j) { return ext[NE ? i : 0][NE ? j : 0]; });
 }
 
 // One 256 x 256 tile on the four-wave main loop (gemm_core_w4.hpp), whose waves
@@ -676,7 +673,7 @@ __global__ __launch_bounds__(kNsThreads, W == 128 && NS > 2 ? 1 : 2) void ns_gem
 // those are bound by LDS bandwidth. One workgroup per CU.
 template <int MODE>
 __global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
-  constexpr bool SYM = MODE == kGram || MODE == kSquare;
+  static_assert(MODE != kSquare, "the square takes narrower tiles");
   constexpr int F = TileW::FM;
   static_assert(TileW::BM == 256 && TileW::BN == 256 && TileW::FN == F && TileW::NT == kNsThreads,
                 "2 x 2 waves of 128 x 128");
@@ -684,11 +681,10 @@ __global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
                 "the output tile is staged in the operands' place");
   __shared__ __attribute__((aligned(16))) char smem_raw[256 * 256 * 2];
   lds_t* smem = (lds_t*)smem_raw;
-  const NsTile tl = ns_tile<SYM>(p);
+  const NsTile tl = ns_tile<MODE == kGram>(p);
   const int row0 = tl.tm * 256, col0 = tl.tn * 256;
   const int64_t ysz = (int64_t)p.cp * p.rp, asz = (int64_t)p.rp * p.rp;
   const char* Y = reinterpret_cast<const char*>(p.y + tl.b * ysz);
-  const char* A = reinterpret_cast<const char*>(p.gram + tl.b * asz);
   const char* Q = reinterpret_cast<const char*>(p.q + tl.b * asz);
   const int64_t ld = (int64_t)p.rp * 2;
   const int na = MODE == kUpdate || MODE == kOutTall ? p.cp : p.rp;
@@ -700,28 +696,10 @@ __global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
     mainloop_w4<Elem::F16, false, TileW, false, true>(smem, Y, ld, row0, na - 1, BDesc{Y, ld, nb},
                                                       col0, PlainCols{col0, nb - 8}, ks, acc);
   } else {
-    const char* a = MODE == kSquare ? A : MODE == kOutWide ? Q : Y;
-    const char* b = MODE == kSquare ? A : MODE == kOutWide ? Y : Q;
+    const char* a = MODE == kOutWide ? Q : Y;
+    const char* b = MODE == kOutWide ? Y : Q;
     mainloop_w4<Elem::F16, true, TileW, false>(smem, a, ld, row0, na - 1, BDesc{b, ld, nb}, col0,
                                                PlainCols{col0, nb - 8}, ks, acc);
-  }
-  if constexpr (MODE == kSquare) {
-    // A's tile, straight into the staged tile's places (loads of 8 bytes per
-    // lane from A's rows took 45 k cycles a tile). A load fills two rows; rows
-    // and columns beyond A load zeros.
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const auto ra = make_rsrc(A + row0 * ld);
-#pragma unroll 4
-    for (int i = 0; i < 32; ++i) {
-      const int r = wave * 64 + i * 2 + (lane >> 5);
-      const int c = (lane & 31) ^ ((r & 15) << 1);
-      const bool in = row0 + r < p.rp && col0 + c * 8 < p.rp;
-      dma16(ra, smem + (wave * 32 + i) * 1024,
-            in ? static_cast<uint32_t>(r * ld + (col0 + c * 8) * 2) : kOffNone);
-    }
-    wait_vmcnt0();
-    __syncthreads();
   }
   // lo, two rows of blocks ahead of its use (the accumulators leave no room to
   // hold it through the main loop)
@@ -735,7 +713,7 @@ __global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
   };
   load(0);
   load(1);
-  ns_epilogue<256, MODE, F, MODE == kSquare>(p, tl, smem, acc, [&](int i, int j) {
+  ns_epilogue<256, MODE, F>(p, tl, smem, acc, [&](int i, int j) {
     if (j == 0 && i + 2 < F) load(i + 2);
     return ext[i % 3][j];
   });
@@ -1075,13 +1053,15 @@ static void ns_start(const void* g, int64_t batch, int64_t m, int64_t n, const N
 // every CU a tile (five steps of 16 x 2048 x 1536: 1.78 ms, with 128 at most
 // 2.02 ms), else 128 where those give every second CU one (one 2048 x 3584: 457 us;
 // asking for one on every CU 477 us, and for one on every third, 3 x 777 x 1001
-// goes from 185 to 227 us), else 64.
+// goes from 185 to 227 us), else 64. The square stays at 128: its K is the short
+// side, and two workgroups per CU hide more of its epilogue (16 x 2048 x 1536 1766
+// against 1805 us; for the Gram product it makes no difference).
 template <int MODE>
 static int ns_plan(NsArgs& p, int64_t batch) {
   constexpr bool SYM = MODE == kGram || MODE == kSquare;
   const int rows = MODE == kUpdate || MODE == kOutTall ? p.cp : p.rp;
   const int cols = MODE == kOutWide ? p.cp : p.rp;
-  for (int w = 256;; w /= 2) {
+  for (int w = MODE == kSquare ? 128 : 256;; w /= 2) {
     p.tiles_m = (rows + w - 1) / w;
     p.tiles_n = (cols + w - 1) / w;
     p.tiles = SYM ? p.tiles_n * (p.tiles_n + 1) / 2 : p.tiles_m * p.tiles_n;
@@ -1098,9 +1078,13 @@ static void ns_product(NsArgs p, int64_t batch, hipStream_t stream) {
   const int w = ns_plan<MODE>(p, batch);
   const int64_t n = batch * p.tiles;
   const dim3 grid(static_cast<unsigned>(n)), blk(kNsThreads);
-  if (w == 256)
-    hipLaunchKernelGGL(ns_gemm256_kernel<MODE>, grid, blk, 0, stream, p);
-  else if (w == 128 && n <= num_cus())
+  if constexpr (MODE != kSquare) {
+    if (w == 256) {
+      hipLaunchKernelGGL(ns_gemm256_kernel<MODE>, grid, blk, 0, stream, p);
+      return;
+    }
+  }
+  if (w == 128 && n <= num_cus())
     hipLaunchKernelGGL((ns_gemm_kernel<128, 4, MODE>), grid, blk, 0, stream, p);
   else if (w == 128)
     hipLaunchKernelGGL((ns_gemm_kernel<128, 2, MODE>), grid, blk, 0, stream, p);
