@@ -1000,6 +1000,30 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
 
 // ---------------------------------------------------------------- host
 
+// Width of a product's tiles, and p's tile counts for it: 256 where those give
+// every CU a tile (five steps of 16 x 2048 x 1536: 1.78 ms, with 128 at most
+// 2.02 ms), else 128 where those give every second CU one (one 2048 x 3584: 457 us;
+// asking for one on every CU 477 us, and for one on every third, 3 x 777 x 1001
+// goes from 185 to 227 us), else 64. The square stays at 128: its K is the short
+// side, and two workgroups per CU hide more of its epilogue (16 x 2048 x 1536 1766
+// against 1805 us; for the Gram product it makes no difference).
+template <int MODE>
+static int ns_plan(NsArgs& p, int64_t batch) {
+  constexpr bool SYM = MODE == kGram || MODE == kSquare;
+  const int rows = MODE == kUpdate || MODE == kOutTall ? p.cp : p.rp;
+  const int cols = MODE == kOutWide ? p.cp : p.rp;
+  for (int w = MODE == kSquare ? 128 : 256;; w /= 2) {
+    p.tiles_m = (rows + w - 1) / w;
+    p.tiles_n = (cols + w - 1) / w;
+    p.tiles = SYM ? p.tiles_n * (p.tiles_n + 1) / 2 : p.tiles_m * p.tiles_n;
+    p.row_tiles = SYM ? p.tiles_n + 1 : p.tiles_n;
+    p.inv_tiles = 1.f / static_cast<float>(p.tiles);
+    p.inv_row_tiles = 1.f / static_cast<float>(p.row_tiles);
+    const int64_t n = batch * p.tiles;
+    if (w == 64 || n >= (w == 256 ? num_cus() : num_cus() / 2)) return w;
+  }
+}
+
 struct NsLayout {
   int64_t r, c, rp, cp;
   size_t part, y0, y1, lo, gram, q, total;
@@ -1017,8 +1041,11 @@ static NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
   L.cp = (L.c + kNsPad - 1) / kNsPad * kNsPad;
   const size_t y = static_cast<size_t>(batch * L.cp * L.rp) * 2;  // multiples of 8 KiB
   const size_t a = static_cast<size_t>(batch * L.rp * L.rp) * 2;
-  // lo in whole tiles of up to 256 x 256
-  const size_t l = static_cast<size_t>(batch * ((L.cp + 255) / 256) * ((L.rp + 255) / 256)) * 256 * 256 * 2;
+  NsArgs p{};
+  p.cp = static_cast<int>(L.cp);
+  p.rp = static_cast<int>(L.rp);
+  const int64_t w = ns_plan<kUpdate>(p, batch);  // lo in whole tiles of the update
+  const size_t l = static_cast<size_t>(batch * p.tiles * w * w) * 2;
   L.part = 0;
   L.y0 = (static_cast<size_t>(batch) * kNsMaxPart * sizeof(double) + 255) / 256 * 256;
   L.y1 = L.y0 + y;
@@ -1047,30 +1074,6 @@ static void ns_start(const void* g, int64_t batch, int64_t m, int64_t n, const N
   };
   if (m >= n) init(ns_init_kernel<D, true>);
   else init(ns_init_kernel<D, false>);
-}
-
-// Width of a product's tiles, and p's tile counts for it: 256 where those give
-// every CU a tile (five steps of 16 x 2048 x 1536: 1.78 ms, with 128 at most
-// 2.02 ms), else 128 where those give every second CU one (one 2048 x 3584: 457 us;
-// asking for one on every CU 477 us, and for one on every third, 3 x 777 x 1001
-// goes from 185 to 227 us), else 64. The square stays at 128: its K is the short
-// side, and two workgroups per CU hide more of its epilogue (16 x 2048 x 1536 1766
-// against 1805 us; for the Gram product it makes no difference).
-template <int MODE>
-static int ns_plan(NsArgs& p, int64_t batch) {
-  constexpr bool SYM = MODE == kGram || MODE == kSquare;
-  const int rows = MODE == kUpdate || MODE == kOutTall ? p.cp : p.rp;
-  const int cols = MODE == kOutWide ? p.cp : p.rp;
-  for (int w = MODE == kSquare ? 128 : 256;; w /= 2) {
-    p.tiles_m = (rows + w - 1) / w;
-    p.tiles_n = (cols + w - 1) / w;
-    p.tiles = SYM ? p.tiles_n * (p.tiles_n + 1) / 2 : p.tiles_m * p.tiles_n;
-    p.row_tiles = SYM ? p.tiles_n + 1 : p.tiles_n;
-    p.inv_tiles = 1.f / static_cast<float>(p.tiles);
-    p.inv_row_tiles = 1.f / static_cast<float>(p.row_tiles);
-    const int64_t n = batch * p.tiles;
-    if (w == 64 || n >= (w == 256 ? num_cus() : num_cus() / 2)) return w;
-  }
 }
 
 template <int MODE>
