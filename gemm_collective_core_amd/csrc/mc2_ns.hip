@@ -733,6 +733,7 @@ __global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
 // 11 us of GPU time, 64 x 1000 and 128 x 512 40 and 60 us.
 constexpr int kTinyThreads = 512;
 constexpr int64_t kTinyElems = 65536;
+constexpr float kTinyScale = kXScale / kUpdScale;  // x's scale, that of hi Q: 2^21
 
 struct TinyArgs {
   const void* g;
@@ -784,6 +785,7 @@ template <int RP, int RB>
 __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
   constexpr int CB = RP / 16, KS = RB * 4;  // 32-row k steps of Y
   constexpr int kGramUnroll = RP == 64 && RB <= 4 ? 4 : 2;  // (registers)
+  constexpr int kUpdUnroll = RP == 64 && RB <= 4 ? 2 : 1;
   constexpr int FA = RP / 64, FB = RP / 32;  // a wave's 16-row / 16-column blocks of A and Q
   __shared__ __attribute__((aligned(16))) char s_y[RB * 128 * RP * 2];
   __shared__ __attribute__((aligned(16))) char s_a[RP * RP * 2];
@@ -831,7 +833,7 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
   double norm2 = 0;
 #pragma unroll
   for (int w = 0; w < kTinyThreads / 64; ++w) norm2 += s_n[w];
-  const double inv = norm2 == 0.0 ? 0.0 : kXScale / (sqrt(norm2) + static_cast<double>(p.eps));
+  const double inv = norm2 == 0.0 ? 0.0 : kTinyScale / (sqrt(norm2) + static_cast<double>(p.eps));
   const float invf = static_cast<float>(inv);
   // in fp64 only where fp32 does not hold 1 / norm (what lies outside G stays
   // zero: inv may be NaN)
@@ -861,8 +863,8 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
     for (int i = 0; i < RB; ++i)
 #pragma unroll
       for (int j = 0; j < CB; ++j)
-        tiny_put<RP>(s_y, (wave * RB + i) * 16 + lr, j * 16 + lc, x[i][j][0], x[i][j][1],
-                     x[i][j][2], x[i][j][3]);
+        tiny_put<RP>(s_y, (wave * RB + i) * 16 + lr, j * 16 + lc, x[i][j][0] * kUpdScale,
+                     x[i][j][1] * kUpdScale, x[i][j][2] * kUpdScale, x[i][j][3] * kUpdScale);
     __syncthreads();
     f32x4_t g[FA][FB];
 #pragma unroll
@@ -925,21 +927,21 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
     __syncthreads();
     // x = a x + (b mu + c mu^2) hi + hi Q: the part of the identity that the
     // product takes away again is added to what the product multiplies, hi (its
-    // rounding would else stay in the directions of singular value zero).
-    // The product's scale is 2^21, x's 2^12.
+    // rounding would else stay in the directions of singular value zero)
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
       for (int j = 0; j < CB; ++j) {
-        // (opaque: hi is formed anew here, not kept in registers from the step's
-        // start)
-        asm volatile("" : "+v"(x[i][j]));
+        // (opaque where registers are short: hi is formed anew here, not kept in
+        // them from the step's start)
+        if constexpr (RB * CB > 8) asm volatile("" : "+v"(x[i][j]));
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[i][j][e] = (a * x[i][j][e] + am * f16_bits_to_f32(f32_to_f16_bits(x[i][j][e]))) *
-                       (1.f / kUpdScale);
+        for (int e = 0; e < 4; ++e) {
+          const float hi = f16_bits_to_f32(f32_to_f16_bits(x[i][j][e] * kUpdScale));
+          x[i][j][e] = __builtin_fmaf(hi, am * (1.f / kUpdScale), a * x[i][j][e]);
+        }
       }
-#pragma unroll 1
+#pragma unroll kUpdUnroll
     for (int ks = 0; ks < RP / 32; ++ks) {
       f16x8_t fa[RB];
 #pragma unroll
@@ -952,18 +954,12 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
           x[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb, fa[i], x[i][j], 0, 0, 0);
       }
     }
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-      for (int j = 0; j < CB; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][j][e] *= kUpdScale;
     // (a wave reads only its own rows of Y above and writes only them in the
     // next step; the reads of Q end before that step's first barrier)
   }
   // The result takes Y's place (a wave's rows are read by that wave alone once Q
   // is formed) and leaves in 16-byte pieces of G's rows (2-byte stores from the registers took 18 us for 128 x 512).
-  const float so = p.scale / kXScale;
+  const float so = p.scale * (1.f / kTinyScale);
   auto stage = [&](auto cvt) {
 #pragma unroll
     for (int i = 0; i < RB; ++i)
