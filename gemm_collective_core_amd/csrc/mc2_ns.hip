@@ -550,20 +550,25 @@ __global__ __launch_bounds__(kNsThreads, W == 128 && NS > 2 ? 1 : 2) void ns_gem
     u32x2_t h[KMAJ ? F : 1][2];
   };
   const uint32_t s0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
-  auto read = [&](Frags& f, uint32_t s, int x0, int ks) {
-#pragma unroll
-    for (int i = 0; i < F; ++i) {
-      if constexpr (KMAJ) {
-        const int j = lane & 15, g = lane >> 4;
-        const int kr = ks * 32 + g * 8 + (j >> 2);
-        const uint32_t at = s + kr * (W * 2) + ((((x0 >> 4) + i) ^ ns_kswz<W>(kr)) << 5) + ((j & 3) << 3);
-        asm volatile("ds_read_b64_tr_b16 %0, %1" : "=v"(f.h[i][0]) : "v"(at) : "memory");
+  // read q (of NR) of k-step ks from the stage at s: B's fragments, then A's
+  auto read = [&](Frags& fa, Frags& fb, uint32_t s, int ks, int q) {
+    constexpr int N = NR / 2;
+    Frags& f = q < N ? fb : fa;
+    const uint32_t base = q < N ? s + OB : s;
+    const int x0 = q < N ? wc : wr, k = q < N ? q : q - N;
+    if constexpr (KMAJ) {
+      const int i = k >> 1, j = lane & 15, g = lane >> 4;
+      const int kr = ks * 32 + g * 8 + (j >> 2);
+      const uint32_t at =
+          base + kr * (W * 2) + ((((x0 >> 4) + i) ^ ns_kswz<W>(kr)) << 5) + ((j & 3) << 3);
+      if (k & 1)
         asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2"
                      : "=v"(f.h[i][1]) : "v"(at), "i"(4 * W * 2) : "memory");
-      } else {
-        const uint32_t at = s + row_off(x0 + i * 16 + (lane & 15), ks * 4 + (lane >> 4));
-        asm volatile("ds_read_b128 %0, %1" : "=v"(f.q[i]) : "v"(at) : "memory");
-      }
+      else
+        asm volatile("ds_read_b64_tr_b16 %0, %1" : "=v"(f.h[i][0]) : "v"(at) : "memory");
+    } else {
+      const uint32_t at = base + row_off(x0 + k * 16 + (lane & 15), ks * 4 + (lane >> 4));
+      asm volatile("ds_read_b128 %0, %1" : "=v"(f.q[k]) : "v"(at) : "memory");
     }
   };
   // ties the fragments to the wait before it: no use of them moves above
@@ -629,16 +634,21 @@ __global__ __launch_bounds__(kNsThreads, W == 128 && NS > 2 ? 1 : 2) void ns_gem
   Frags a0, b0, a1, b1;
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 1) * 2 * NL) : "memory");
   bar_sync();
-  read(b0, s0 + OB, wc, 0);
-  read(a0, s0, wr, 0);
+#pragma unroll
+  for (int q = 0; q < NR; ++q) read(a0, b0, s0, 0, q);
+  // One MFMA, then up to two LDS reads and one load: a memory instruction that
+  // waits to be taken then costs no more than the MFMAs in flight, and with one
+  // workgroup per CU nobody else would fill that time.
   for (int s = 0; s < stages; ++s) {
     const uint32_t sa = s0 + (s % NS) * 2 * OB, sn = s0 + ((s + 1) % NS) * 2 * OB;
-    read(b1, sa + OB, wc, 1);
-    read(a1, sa, wr, 1);
-    lgkm_wait(NR);
+    lgkm_wait(0);
     tie(b0);
     tie(a0);
-    multiply(a0, b0, [](int) {});
+    multiply(a0, b0, [&](int q) {
+#pragma unroll
+      for (int r = 2 * q; r < 2 * q + 2; ++r)
+        if (r < NR) read(a1, b1, sa, 1, r);
+    });
     // every read of this stage is done, by every wave: its buffer may be
     // filled again; and the next stage has landed (this wave's loads of it,
     // those of later stages may be in flight: loads complete in order; then
@@ -651,10 +661,11 @@ __global__ __launch_bounds__(kNsThreads, W == 128 && NS > 2 ? 1 : 2) void ns_gem
     // under the second k-step's products: the next stage's first fragments
     // (after the last stage: of a buffer nobody fills any more, never used),
     // and the loads of stage s + NS
-    read(b0, sn + OB, wc, 0);
-    read(a0, sn, wr, 0);
     const Stage st = stage_of(s + NS);
     multiply(a1, b1, [&](int q) {
+#pragma unroll
+      for (int r = 2 * q; r < 2 * q + 2; ++r)
+        if (r < NR) read(a0, b0, sn, 0, r);
       constexpr int kEvery = F * F / (2 * NL);
       if (q % kEvery == kEvery - 1) issue(st, q / kEvery);
     });
