@@ -460,7 +460,8 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
 // W = 128, NS = 4 is for launches of at most one workgroup per CU, which has
 // nobody to hide its loads' latency. The 128 x 128 tiles are bound by LDS
 // bandwidth (96 KiB per stage, 768 cycles against 512 of MFMA), the 64 x 64
-// ones by their start and end (2500 cycles against 250 to 300 a stage).
+// ones by the CU's load path (16 KiB per stage, about 450 cycles against 128 of
+// MFMA) and, in short contractions, by their start and end (4500 cycles).
 // Each MFMA takes the second operand's fragment first, so a lane ends with
 // four consecutive columns of one row.
 template <int W, int NS, int MODE>
@@ -741,7 +742,9 @@ __global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
 // registers, in the accumulator layout: the product Y Q is added onto a Y held
 // there, so no low half is needed, and a wave's update touches its own rows
 // only. A (less mu I) and Q take turns in one (rp, rp) LDS array. 64 x 256 takes
-// 11 us of GPU time, 64 x 1000 and 128 x 512 40 and 60 us.
+// 16 us (65 as 17 launches): 35 k cycles, of them 8 k until the first product,
+// 2100 a step for the Gram product (LDS bandwidth) and 2100 for the update;
+// 64 x 1000 takes 54 us and 128 x 512 67 us.
 constexpr int kTinyThreads = 512;
 constexpr int64_t kTinyElems = 65536;
 constexpr float kTinyScale = kXScale / kUpdScale;  // x's scale, that of hi Q: 2^21
