@@ -224,3 +224,33 @@ def test_permute_kernels_indices_fit():
     n = int(offs[E].item())
     assert n == T * K - 1 and err.item() == 0
     assert (dy[n:] == 9.0).all() and not (dy[:n] == 9.0).all(1).any()
+
+
+def test_offsets_beyond_32_bits():
+    """Row buffers of more than 2^31 elements: rows near the end are found."""
+    T, K, H = 131080, 8, 2056
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    uidx = torch.randperm(T * K, generator=gen, device="cuda")
+    sidx = torch.empty_like(uidx)
+    sidx[uidx] = torch.arange(T * K, device="cuda")
+    u32, s32 = uidx.to(torch.int32), sidx.to(torch.int32)
+    y = torch.randn((T * K, H), generator=gen, device="cuda", dtype=BF)
+    assert y.numel() > 2 ** 31
+    dout = torch.randn((T, H), generator=gen, device="cuda", dtype=BF)
+    probs = torch.rand((T, K), generator=gen, device="cuda")
+    err = _err()
+    dy, dp = mc2.mc2_moe_unpermute_backward(dout, y, u32, s32, probs, dev_err=err)
+    dx = mc2.mc2_moe_permute_backward(y, u32, K, dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    rows = torch.cat([torch.arange(4, device="cuda"), torch.arange(T * K - 60, T * K, device="cuda")])
+    s = sidx[rows]
+    d, yr = dout[s // K].double(), y[rows].double()
+    ref = probs.view(-1)[s][:, None].double() * d
+    assert ((dy[rows].double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -24) * ref.abs() + 1e-38).all()
+    tol = (H + 8) * 2.0 ** -24 * (d * yr).abs().sum(1)
+    assert ((dp.view(-1)[s].double() - (d * yr).sum(1)).abs() <= tol).all()
+    t = s // K
+    mine = y[uidx.view(T, K)[t]].double()
+    tol = 2.0 ** -8 * mine.sum(1).abs() + (K + 1) * 2.0 ** -23 * mine.abs().sum(1)
+    assert ((dx[t].double() - mine.sum(1)).abs() <= tol).all()

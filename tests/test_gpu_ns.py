@@ -61,7 +61,7 @@ def test_sizes_and_types(B, m, n, dt, out):
     _check(g, o)
 
 
-@pytest.mark.parametrize("m,n", [(192, 320), (320, 192), (777, 1001)])
+@pytest.mark.parametrize("m,n", [(192, 320), (320, 192), (777, 1001), (60, 250), (500, 120)])
 @pytest.mark.parametrize("rank", [1, 16, 100])
 def test_rank_deficient(m, n, rank):
     """An expert with fewer tokens than its matrix has rows: the other singular
@@ -156,3 +156,34 @@ def test_captured_and_replayed(B, m, n):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(o.view(torch.int16), eager[i].view(torch.int16)), i
+
+
+@pytest.mark.parametrize("B,m,n", [(1, 3, 65536), (1, 65536, 5), (1, 130, 20000), (65535, 1, 2),
+                                   (300, 130, 190), (1, 2500, 2500)])
+def test_long_thin_and_many(B, m, n):
+    """The largest sides and stacks, and a square matrix wider than a round of
+    tiles; some matrices of a large stack stand for all."""
+    g = torch.randn((B, m, n), generator=torch.Generator().manual_seed(6)).cuda()
+    o = mc2.mc2_ns_orthogonalize(g)
+    torch.cuda.synchronize()
+    pick = sorted({0, B // 2, B - 1})
+    _check(g[pick], o[pick])
+
+
+@pytest.mark.parametrize("m,n", [(50, 120), (120, 50), (200, 136)])
+def test_in_place(m, n):
+    g = torch.randn((3, m, n), generator=torch.Generator().manual_seed(7)).to(BF).cuda()
+    ref = mc2.mc2_ns_orthogonalize(g)
+    assert mc2.mc2_ns_orthogonalize(g, out=g) is g
+    assert torch.equal(g.view(torch.int16), ref.view(torch.int16))
+
+
+@pytest.mark.parametrize("m,n", [(50, 120), (200, 136)])
+def test_iterates_out_of_range_end_as_such(m, n):
+    """Coefficients whose iterates grow without bound: infinities or NaN, and a
+    matrix of zeros beside it stays zero."""
+    g = torch.randn((2, m, n), generator=torch.Generator().manual_seed(8)).cuda()
+    g[1] = 0
+    o = mc2.mc2_ns_orthogonalize(g, steps=32, coeffs=(16.0, 16.0, 16.0))
+    torch.cuda.synchronize()
+    assert not torch.isfinite(o[0]).any() and (o[1] == 0).all()
