@@ -423,14 +423,16 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
     __syncthreads();
     store(p.ynext + b * ysz, p.rp, p.cp, p.rp);
   } else {
-    const float sc = p.scale * kOutScale;
+    // (the power of two first, which is exact: the factor of both is not for a
+    // scale near the smallest numbers)
+    auto scaled = [&](float v) { return v * kOutScale * p.scale; };
     auto stage = [&](auto cvt) {
 #pragma unroll
       for (int i = 0; i < F; ++i)
 #pragma unroll
         for (int j = 0; j < F; ++j)
-          *place(i, j) = u32x2_t{cvt(acc[i][j][0] * sc, acc[i][j][1] * sc),
-                                 cvt(acc[i][j][2] * sc, acc[i][j][3] * sc)};
+          *place(i, j) = u32x2_t{cvt(scaled(acc[i][j][0]), scaled(acc[i][j][1])),
+                                 cvt(scaled(acc[i][j][2]), scaled(acc[i][j][3]))};
     };
     if (p.out_bf16)
       stage([](float x, float y) {
@@ -973,7 +975,6 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
   }
   // The result takes Y's place (a wave's rows are read by that wave alone once Q
   // is formed) and leaves in 16-byte pieces of G's rows (2-byte stores from the registers took 18 us for 128 x 512).
-  const float so = p.scale * (1.f / kTinyScale);
   auto stage = [&](auto cvt) {
 #pragma unroll
     for (int i = 0; i < RB; ++i)
@@ -982,7 +983,7 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
         const int row = (wave * RB + i) * 16 + lr, col = j * 16 + lc;
         uint32_t h[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = cvt(x[i][j][e] * so);
+        for (int e = 0; e < 4; ++e) h[e] = cvt(x[i][j][e] * (1.f / kTinyScale) * p.scale);
         *reinterpret_cast<u32x2_t*>(s_y + tiny_pos<RP>(row, col >> 3) + ((col & 4) << 1)) =
             u32x2_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
       }
