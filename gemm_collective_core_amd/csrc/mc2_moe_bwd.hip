@@ -200,11 +200,11 @@ template <bool F16, int LPR, int C>
 __global__ __launch_bounds__(kBwdThreads) void unpermute_bwd_kernel(
     const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y, int64_t p_end,
     const int32_t* __restrict__ idx, const int32_t* __restrict__ sorted,
-    const float* __restrict__ probs, int64_t T, int K, int64_t H, uint16_t* __restrict__ dy,
-    float* __restrict__ dprobs, uint32_t readers, int32_t* dev_err) {
+    const float* __restrict__ probs, int64_t t0, int64_t T, int K, int64_t H,
+    uint16_t* __restrict__ dy, float* __restrict__ dprobs, uint32_t readers, int32_t* dev_err) {
   const bool reads = blockIdx.x < readers;
   const int64_t blk = reads ? blockIdx.x : blockIdx.x - readers;
-  const int64_t t = blk * (kBwdThreads / LPR) + threadIdx.x / LPR;
+  const int64_t t = t0 + blk * (kBwdThreads / LPR) + threadIdx.x / LPR;
   if (t >= T) return;
   const bool bad = reads ? probs_grad<F16, LPR, C>(dout, y, p_end, idx, sorted, t, K, H, dprobs)
                          : rows_grad<F16, LPR, C>(dout, p_end, idx, sorted, probs, t, K, H, dy);
@@ -215,10 +215,10 @@ __global__ __launch_bounds__(kBwdThreads) void unpermute_bwd_kernel(
 // gather without weights.
 template <bool F16, int LPR, int C>
 __global__ __launch_bounds__(kBwdThreads) void permute_bwd_kernel(
-    const uint16_t* __restrict__ g, int64_t rows, const int32_t* __restrict__ idx, int64_t T,
-    int K, int64_t H, uint16_t* __restrict__ dx, int32_t* dev_err) {
+    const uint16_t* __restrict__ g, int64_t rows, const int32_t* __restrict__ idx, int64_t t0,
+    int64_t T, int K, int64_t H, uint16_t* __restrict__ dx, int32_t* dev_err) {
   const int gl = threadIdx.x & (LPR - 1);
-  const int64_t t = (int64_t)blockIdx.x * (kBwdThreads / LPR) + threadIdx.x / LPR;
+  const int64_t t = t0 + (int64_t)blockIdx.x * (kBwdThreads / LPR) + threadIdx.x / LPR;
   if (t >= T) return;
   const int64_t CR = H / 8;
   bool bad = false;
@@ -293,6 +293,18 @@ static void for_rows(int dtype, int64_t H, F&& f) {
   else with(std::false_type{});
 }
 
+// Calls f(t0, workgroups) for token ranges that cover T tokens, `per` of them a
+// workgroup: a launch holds fewer than 2^32 threads, 2^31 are taken with up to
+// two workgroups for the same tokens.
+constexpr int64_t kMaxRangeBlocks = (int64_t{1} << 30) / kBwdThreads;
+template <class F>
+static void for_ranges(int64_t T, int per, F&& f) {
+  for (int64_t t0 = 0; t0 < T; t0 += kMaxRangeBlocks * per) {
+    const int64_t blocks = (T - t0 + per - 1) / per;
+    f(t0, static_cast<unsigned>(blocks < kMaxRangeBlocks ? blocks : kMaxRangeBlocks));
+  }
+}
+
 static int check_rows(int64_t T, int K, int64_t H, int64_t rows, int dtype) {
   if (dtype != MC2_BF16 && dtype != MC2_F16) return MC2_ERR_DTYPE;
   if (T < 1 || K < 1 || K > 64 || H < 8 || rows < 0) return MC2_ERR_SHAPE;
@@ -317,14 +329,14 @@ extern "C" int mc2_moe_unpermute_backward(const void* dout, const void* y_full, 
   const int64_t p_end = y_rows < T * K ? y_rows : T * K;
   for_rows(dtype, H, [&](auto half, auto lpr, auto c) {
     constexpr int LPR = decltype(lpr)::value;
-    constexpr int per = kBwdThreads / LPR;  // tokens per workgroup
-    const unsigned grid = static_cast<unsigned>((T + per - 1) / per);
-    const unsigned readers = dprobs ? grid : 0u;
-    hipLaunchKernelGGL((unpermute_bwd_kernel<decltype(half)::value, LPR, decltype(c)::value>),
-                       dim3(readers + (dy ? grid : 0u)), dim3(kBwdThreads), 0, stream,
-                       static_cast<const uint16_t*>(dout),
-                       static_cast<const uint16_t*>(y_full), p_end, unpermute_idx, sorted_idx,
-                       probs, T, K, H, static_cast<uint16_t*>(dy), dprobs, readers, dev_err);
+    for_ranges(T, kBwdThreads / LPR, [&](int64_t t0, unsigned grid) {
+      const unsigned readers = dprobs ? grid : 0u;
+      hipLaunchKernelGGL((unpermute_bwd_kernel<decltype(half)::value, LPR, decltype(c)::value>),
+                         dim3(readers + (dy ? grid : 0u)), dim3(kBwdThreads), 0, stream,
+                         static_cast<const uint16_t*>(dout),
+                         static_cast<const uint16_t*>(y_full), p_end, unpermute_idx, sorted_idx,
+                         probs, t0, T, K, H, static_cast<uint16_t*>(dy), dprobs, readers, dev_err);
+    });
   });
   return hipGetLastError() == hipSuccess ? MC2_OK : MC2_ERR_HIP;
 }
@@ -339,11 +351,12 @@ extern "C" int mc2_moe_permute_backward(const void* dpermuted, int64_t rows,
   if (!aligned16(dpermuted) || !aligned16(dx)) return MC2_ERR_ALIGN;
   for_rows(dtype, H, [&](auto half, auto lpr, auto c) {
     constexpr int LPR = decltype(lpr)::value;
-    constexpr int per = kBwdThreads / LPR;
-    hipLaunchKernelGGL((permute_bwd_kernel<decltype(half)::value, LPR, decltype(c)::value>),
-                       dim3(static_cast<unsigned>((T + per - 1) / per)), dim3(kBwdThreads), 0,
-                       stream, static_cast<const uint16_t*>(dpermuted), rows, unpermute_idx, T, K,
-                       H, static_cast<uint16_t*>(dx), dev_err);
+    for_ranges(T, kBwdThreads / LPR, [&](int64_t t0, unsigned grid) {
+      hipLaunchKernelGGL((permute_bwd_kernel<decltype(half)::value, LPR, decltype(c)::value>),
+                         dim3(grid), dim3(kBwdThreads), 0, stream,
+                         static_cast<const uint16_t*>(dpermuted), rows, unpermute_idx, t0, T, K, H,
+                         static_cast<uint16_t*>(dx), dev_err);
+    });
   });
   return hipGetLastError() == hipSuccess ? MC2_OK : MC2_ERR_HIP;
 }
