@@ -345,7 +345,7 @@ extern "C" int mc2_moe_permute_backward(const void* dpermuted, int64_t rows,
                                         const int32_t* unpermute_idx, int64_t T, int K, int64_t H,
                                         int dtype, void* dx, int32_t* dev_err,
                                         hipStream_t stream) {
-  if (!dpermuted || !unpermute_idx || !dx) return MC2_ERR_NULL;
+  if ((!dpermuted && rows != 0) || !unpermute_idx || !dx) return MC2_ERR_NULL;
   const int st = check_rows(T, K, H, rows, dtype);
   if (st) return st;
   if (!aligned16(dpermuted) || !aligned16(dx)) return MC2_ERR_ALIGN;

@@ -58,7 +58,8 @@ int mc2_moe_unpermute_backward(const void* dout, const void* y_full, int64_t y_r
  * -1 or >= rows is skipped and sets MC2_DEVERR_INDEX. This is a gather: an
  * index may appear more than once.
  *   dpermuted (rows, H), dx (T, H): dtype, MC2_BF16 or MC2_F16;
- *   unpermute_idx (T*K) int32. dx must not overlap dpermuted.
+ *   unpermute_idx (T*K) int32. dx must not overlap dpermuted, which may be
+ *   NULL where rows is 0 (a rank that got no rows: dx is zeros).
  * Constraints: T >= 1, 1 <= K <= 64, H >= 8, H % 8 == 0, T*K < 2^31 - 1,
  * rows >= 0.
  */

@@ -49,3 +49,18 @@ def test_permute_backward_of_more_tokens_than_one_launch_holds():
     step = 2 ** 22  # (torch's own indexing has a smaller limit)
     for t in range(0, T, step):
         assert torch.equal(dx[t:t + step], g[idx[t:t + step].long()])
+
+
+@pytest.mark.parametrize("named", [False, True])
+def test_permute_backward_without_rows(named):
+    """A rank whose row buffer is empty: every token's gradient is zero, and a
+    slot that names a row all the same is reported."""
+    T, K, H = 21, 3, 72
+    idx = torch.full((T * K,), -1, dtype=torch.int32, device="cuda")
+    if named:
+        idx[17] = 0
+    err = _err()
+    dx = mc2.mc2_moe_permute_backward(torch.empty((0, H), dtype=BF, device="cuda"), idx, K,
+                                      dx=torch.ones((T, H), dtype=BF, device="cuda"), dev_err=err)
+    torch.cuda.synchronize()
+    assert (dx == 0).all() and err.item() == (mc2.MC2_DEVERR_INDEX if named else 0)
