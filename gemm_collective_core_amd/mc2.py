@@ -540,29 +540,41 @@ def mc2_moe_unpermute_backward(dout, y_full, unpermute_idx, sorted_idx, probs, *
     of one that is not needed. dy (rows of y_full, H) gets the rows that the
     slots name; its other rows are left as they were (undefined where dy is
     allocated here). sorted_idx and unpermute_idx are mc2_moe_permute's.
-    dprobs (T, K) fp32."""
-    if probs.dim() != 2 or dout.dim() != 2 or y_full.dim() != 2:
-        raise ValueError("probs must be (T, K), dout (T, H) and y_full (rows, H)")
+    dprobs (T, K) fp32. What is not read may be None: probs without need_dy,
+    y_full without need_dprobs where dy is given. y_full and dy have one row at
+    least."""
     if not (need_dy or need_dprobs):
         raise ValueError("nothing to compute: need_dy and need_dprobs are both false")
-    T, K = probs.shape
-    H = dout.shape[1]
+    rows = dy if y_full is None else y_full
+    if rows is None or (need_dprobs and y_full is None):
+        raise ValueError("y_full is needed for dprobs, and where no dy is given")
+    if probs is None and need_dy:
+        raise ValueError("probs is needed for dy")
+    if dout.dim() != 2 or rows.dim() != 2 or (probs is not None and probs.dim() != 2):
+        raise ValueError("probs must be (T, K), dout (T, H) and y_full (rows, H)")
+    T, H = dout.shape
+    if probs is not None:
+        T, K = probs.shape
+    elif T and unpermute_idx.numel() % T == 0:
+        K = unpermute_idx.numel() // T
+    else:
+        raise ValueError("unpermute_idx must hold T * K elements")
     _want(dout, "dout", shape=(T, H), dtypes=_FLOAT16)
-    _want(y_full, "y_full", shape=(y_full.shape[0], H), dtype=dout.dtype)
+    _want(y_full, "y_full", shape=(rows.shape[0], H), dtype=dout.dtype)
     _want(probs, "probs", dtype=torch.float32)
     _want(unpermute_idx, "unpermute_idx", dtype=torch.int32, numel=T * K)
     _want(sorted_idx, "sorted_idx", dtype=torch.int32, numel=T * K)
-    _want(dy, "dy", shape=y_full.shape, dtype=dout.dtype)
+    _want(dy, "dy", shape=(rows.shape[0], H), dtype=dout.dtype)
     _want(dprobs, "dprobs", shape=(T, K), dtype=torch.float32)
     _want(dev_err, "dev_err", **_ERR)
     dev = _dev(dout, y_full, unpermute_idx, sorted_idx, probs, dy, dprobs, dev_err)
-    dy = (torch.empty_like(y_full) if dy is None else dy) if need_dy else None
+    dy = (torch.empty_like(rows) if dy is None else dy) if need_dy else None
     if need_dprobs and dprobs is None:
         dprobs = torch.empty((T, K), dtype=torch.float32, device=dev)
     dprobs = dprobs if need_dprobs else None
-    st = _call(dev, _lib.load().mc2_moe_unpermute_backward, dout.data_ptr(), y_full.data_ptr(),
-               y_full.shape[0], unpermute_idx.data_ptr(), sorted_idx.data_ptr(),
-               probs.data_ptr(), T, K, H, _CODES[dout.dtype], _ptr(dy), _ptr(dprobs),
+    st = _call(dev, _lib.load().mc2_moe_unpermute_backward, dout.data_ptr(), _ptr(y_full),
+               rows.shape[0], unpermute_idx.data_ptr(), sorted_idx.data_ptr(),
+               _ptr(probs), T, K, H, _CODES[dout.dtype], _ptr(dy), _ptr(dprobs),
                _ptr(dev_err), _stream(dev))
     _check("mc2_moe_unpermute_backward", st)
     return dy, dprobs

@@ -64,3 +64,18 @@ def test_permute_backward_without_rows(named):
                                       dx=torch.ones((T, H), dtype=BF, device="cuda"), dev_err=err)
     torch.cuda.synchronize()
     assert (dx == 0).all() and err.item() == (mc2.MC2_DEVERR_INDEX if named else 0)
+
+
+def test_unpermute_backward_without_what_it_does_not_read():
+    T, K, H = 40, 4, 136
+    idx = torch.randperm(T * K, device="cuda").to(torch.int32)
+    sidx = torch.empty_like(idx)
+    sidx[idx.long()] = torch.arange(T * K, dtype=torch.int32, device="cuda")
+    dout, y = _ints((T, H), 5), _ints((T * K, H), 6)
+    probs = torch.exp2(_ints((T, K), 7).float())
+    dy, dp = mc2.mc2_moe_unpermute_backward(dout, y, idx, sidx, probs)
+    got, none = mc2.mc2_moe_unpermute_backward(dout, None, idx, sidx, probs,
+                                               dy=torch.zeros_like(dy), need_dprobs=False)
+    assert none is None and torch.equal(got, dy)
+    none, got = mc2.mc2_moe_unpermute_backward(dout, y, idx, sidx, None, need_dy=False)
+    assert none is None and torch.equal(got, dp)
