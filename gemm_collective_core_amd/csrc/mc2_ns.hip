@@ -1012,6 +1012,11 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
 
 // ---------------------------------------------------------------- host
 
+// The widest tiles that a matrix takes: none of twice its padded smaller side,
+// of which half would be padding (five steps of 256 x 64 x 2048: 426 us, with
+// 256 wide ones 922; 64 x 72 x 1300: 163 and 223; lo is as much smaller).
+static int ns_widest(int64_t rp) { return rp <= 64 ? 64 : rp <= 128 ? 128 : 256; }
+
 // Width of a product's tiles, and p's tile counts for it: 256 where those give
 // every CU a tile (five steps of 16 x 2048 x 1536: 1.78 ms, with 128 at most
 // 2.02 ms), else 128 where those give every second CU one (one 2048 x 3584: 457 us;
@@ -1024,7 +1029,8 @@ static int ns_plan(NsArgs& p, int64_t batch) {
   constexpr bool SYM = MODE == kGram || MODE == kSquare;
   const int rows = MODE == kUpdate || MODE == kOutTall ? p.cp : p.rp;
   const int cols = MODE == kOutWide ? p.cp : p.rp;
-  for (int w = MODE == kSquare ? 128 : 256;; w /= 2) {
+  const int widest = ns_widest(p.rp);
+  for (int w = MODE == kSquare && widest > 128 ? 128 : widest;; w /= 2) {
     p.tiles_m = (rows + w - 1) / w;
     p.tiles_n = (cols + w - 1) / w;
     p.tiles = SYM ? p.tiles_n * (p.tiles_n + 1) / 2 : p.tiles_m * p.tiles_n;
@@ -1045,19 +1051,32 @@ static bool ns_sizes_ok(int64_t batch, int64_t m, int64_t n) {
   return batch >= 1 && batch <= 65535 && m >= 1 && n >= 1 && m <= 65536 && n <= 65536;
 }
 
+// Rows per wave (in blocks of 16, a power of two) of ns_tiny_kernel for a matrix
+// that one workgroup can hold, else 0.
+static int ns_tiny_rows(int64_t rp, int64_t cp) {
+  int rb = 1;
+  while (rb * 128 < cp) rb *= 2;
+  return rp <= 128 && rb * 128 * rp <= kTinyElems ? rb : 0;
+}
+
+// The workspace, from the sizes alone. Matrices that one workgroup holds use
+// none of it: theirs is that of one matrix, whatever the batch.
 static NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
   NsLayout L{};
   L.r = m < n ? m : n;
   L.c = m < n ? n : m;
   L.rp = (L.r + kNsPad - 1) / kNsPad * kNsPad;
   L.cp = (L.c + kNsPad - 1) / kNsPad * kNsPad;
+  if (ns_tiny_rows(L.rp, L.cp)) batch = 1;
   const size_t y = static_cast<size_t>(batch * L.cp * L.rp) * 2;  // multiples of 8 KiB
   const size_t a = static_cast<size_t>(batch * L.rp * L.rp) * 2;
-  NsArgs p{};
-  p.cp = static_cast<int>(L.cp);
-  p.rp = static_cast<int>(L.rp);
-  const int64_t w = ns_plan<kUpdate>(p, batch);  // lo in whole tiles of the update
-  const size_t l = static_cast<size_t>(batch * p.tiles * w * w) * 2;
+  // lo in whole tiles of the update, of any width that it may take
+  int64_t most = 0;
+  for (int64_t w = 64; w <= ns_widest(L.rp); w *= 2) {
+    const int64_t places = (L.cp + w - 1) / w * w * ((L.rp + w - 1) / w * w);
+    most = most > places ? most : places;
+  }
+  const size_t l = static_cast<size_t>(batch * most) * 2;
   L.part = 0;
   L.y0 = (static_cast<size_t>(batch) * kNsMaxPart * sizeof(double) + 255) / 256 * 256;
   L.y1 = L.y0 + y;
@@ -1110,20 +1129,18 @@ static void ns_product(NsArgs p, int64_t batch, hipStream_t stream) {
 // The whole call as one launch, for matrices that one workgroup can hold.
 // Returns false for others.
 static bool ns_tiny(const TinyArgs& p, int64_t batch, const NsLayout& L, hipStream_t stream) {
-  const int64_t rb = (L.cp + 127) / 128;
-  int64_t pow2 = 1;
-  while (pow2 < rb) pow2 *= 2;
-  if (L.rp > 128 || pow2 * 128 * L.rp > kTinyElems) return false;
+  const int rb = ns_tiny_rows(L.rp, L.cp);
+  if (rb == 0) return false;
   const dim3 grid(static_cast<unsigned>(batch)), blk(kTinyThreads);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, blk, 0, stream, p); };
   if (L.rp == 64) {
-    if (pow2 == 1) go(ns_tiny_kernel<64, 1>);
-    else if (pow2 == 2) go(ns_tiny_kernel<64, 2>);
-    else if (pow2 == 4) go(ns_tiny_kernel<64, 4>);
+    if (rb == 1) go(ns_tiny_kernel<64, 1>);
+    else if (rb == 2) go(ns_tiny_kernel<64, 2>);
+    else if (rb == 4) go(ns_tiny_kernel<64, 4>);
     else go(ns_tiny_kernel<64, 8>);
   } else {
-    if (pow2 == 1) go(ns_tiny_kernel<128, 1>);
-    else if (pow2 == 2) go(ns_tiny_kernel<128, 2>);
+    if (rb == 1) go(ns_tiny_kernel<128, 1>);
+    else if (rb == 2) go(ns_tiny_kernel<128, 2>);
     else go(ns_tiny_kernel<128, 4>);
   }
   return true;

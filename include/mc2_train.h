@@ -87,7 +87,11 @@ int mc2_moe_permute_backward(const void* dpermuted, int64_t rows, const int32_t*
  *     two types have the same size; otherwise they must not overlap.
  *   workspace: caller-owned, 16-byte aligned, at least
  *     mc2_ns_workspace_size(batch, m, n) bytes, no initialisation needed.
- *     Calls that overlap in time must not share one.
+ *     Calls that overlap in time must not share one. The size follows from the
+ *     arguments alone, not from the device: batch times that of one matrix, or
+ *     that of one matrix whatever the batch where one workgroup iterates a
+ *     matrix (r padded to 64 at most 128, and at most 64 Ki elements with c
+ *     padded to a power of two times 128).
  * Constraints: 1 <= batch <= 65535, 1 <= m, n <= 65536 (any sizes: rows need
  * not be whole 16-byte pieces); mc2_ns_workspace_size gives 0 for sizes outside.
  * batch * ceil(m / 64) * ceil(n / 64) < 2^24 (128 GiB for one copy of the

@@ -3,6 +3,9 @@ import pytest
 import torch
 
 from gemm_collective_core_amd import mc2
+from oracle import ns_rounding as nr
+from oracle import train as ot
+from test_ns_rounding import SPREAD, rel
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +27,23 @@ def test_scales_near_the_ends_of_the_range(m, n, scale):
     assert ((got.diagonal() - scale * one).abs() <= 2.1 * 2.0 ** -8 * abs(scale) * one).all()
     got.fill_diagonal_(0)
     assert (got == 0).all()
+
+
+@pytest.mark.parametrize("B,m,n", [(1, 3, 65536), (60, 64, 1088), (3, 100, 700), (300, 130, 190),
+                                   (16, 300, 2000), (5, 2000, 300), (40, 64, 256)])
+def test_nothing_behind_the_workspace_is_written(B, m, n):
+    """Tiles of every width, in a workspace of exactly the size asked for."""
+    g = torch.randn((B, m, n), generator=torch.Generator().manual_seed(9)).cuda()
+    ref = mc2.mc2_ns_orthogonalize(g)
+    need = mc2.mc2_ns_workspace_size(B, m, n)
+    buf = torch.full((need + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    out = mc2.mc2_ns_orthogonalize(g, workspace=buf[:need])
+    torch.cuda.synchronize()
+    assert (buf[need:] == 0xAB).all()
+    assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
+    pick = sorted({0, B - 1})
+    for b in pick:
+        want = ot.newton_schulz(g[b].double().cpu().numpy(), (mc2.MC2_NS_COEFFS,) * 5, 1e-7, 1.0)
+        tol = SPREAD * nr.typical(g[b].double().cpu().numpy(), (mc2.MC2_NS_COEFFS,) * 5)
+        if min(m, n) >= 48:  # (of three rows, roundings do not average out)
+            assert rel(out[b].double().cpu().numpy(), want) <= tol + 2.0 ** -8

@@ -35,3 +35,26 @@ def test_unpermute_backward(args, kw, match):
     y, idx, probs = args
     with pytest.raises(ValueError, match=match):
         mc2.mc2_moe_unpermute_backward(DOUT, y, idx, IDX, probs, **kw)
+
+
+@pytest.mark.parametrize("m,n", [(200, 304), (1100, 64), (130, 20000), (777, 1001), (3, 65536)])
+def test_ns_workspace_grows_with_the_batch_alone(m, n):
+    """The size is a matter of the sizes, not of how many tiles fill a device."""
+    f = mc2.mc2_ns_workspace_size
+    one = f(1, m, n)
+    for batch in (2, 17, 300, 2000):
+        assert f(batch, m, n) == batch * one
+    # two iterates, the low half (in whole tiles of at most twice the smaller
+    # side), two (r, r) matrices and the partial norms
+    rp, cp = (-(-v // 64) * 64 for v in (min(m, n), max(m, n)))
+    w = 64 if rp <= 64 else 128 if rp <= 128 else 256
+    lo = -(-rp // w) * w * (-(-cp // w) * w)
+    assert one <= (2 * rp * cp + lo + 2 * rp * rp) * 2 + 2048
+    assert lo <= 2 * rp * cp or cp < w
+
+
+@pytest.mark.parametrize("m,n", [(1, 2), (64, 256), (1024, 64), (128, 512)])
+def test_ns_workspace_of_matrices_in_one_workgroup(m, n):
+    """They use none: it does not grow with the batch."""
+    f = mc2.mc2_ns_workspace_size
+    assert 0 < f(1, m, n) == f(65535, m, n) < 1 << 20
