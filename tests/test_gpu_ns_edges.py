@@ -47,3 +47,37 @@ def test_nothing_behind_the_workspace_is_written(B, m, n):
         tol = SPREAD * nr.typical(g[b].double().cpu().numpy(), (mc2.MC2_NS_COEFFS,) * 5)
         if min(m, n) >= 48:  # (of three rows, roundings do not average out)
             assert rel(out[b].double().cpu().numpy(), want) <= tol + 2.0 ** -8
+
+
+def _typical_error(g, out, steps=5):
+    co = (mc2.MC2_NS_COEFFS,) * steps
+    g = g.double().cpu().numpy()
+    e = rel(out.double().cpu().numpy(), ot.newton_schulz(g, co, 1e-7, 1.0))
+    assert e <= SPREAD * nr.typical(g, co) + nr.HALF
+
+
+@pytest.mark.parametrize("B,m,n", [
+    # one workgroup a matrix: r padded to 64 and 128, c to 128 .. 1024
+    (2, 100, 50), (2, 60, 250), (3, 500, 48), (2, 50, 900), (2, 128, 100), (2, 100, 250),
+    (2, 500, 120),
+    # tiles of 64; of 128, one and several rounds of them; of 256: every product
+    (3, 200, 260), (3, 260, 200), (24, 200, 300), (24, 300, 200), (40, 260, 300), (40, 300, 260),
+    (64, 384, 500), (90, 513, 260), (90, 264, 520)])
+def test_every_kernel(B, m, n):
+    g = torch.randn((B, m, n), generator=torch.Generator().manual_seed(B)).cuda()
+    out = mc2.mc2_ns_orthogonalize(g, out_dtype=torch.float16)
+    torch.cuda.synchronize()
+    for b in sorted({0, B // 2, B - 1}):
+        _typical_error(g[b], out[b])
+
+
+def test_offsets_beyond_32_bits():
+    """A stack of more than 2^31 elements."""
+    B, m, n = 520, 2048, 2050
+    g = torch.randn((B, m, n), generator=torch.Generator(device="cuda").manual_seed(3),
+                    device="cuda")
+    assert g.numel() > 2 ** 31
+    out = mc2.mc2_ns_orthogonalize(g, steps=1, out_dtype=torch.float16)
+    torch.cuda.synchronize()
+    for b in (0, B - 1):
+        _typical_error(g[b], out[b], 1)
