@@ -193,9 +193,9 @@ __device__ __forceinline__ bool rows_grad(const uint16_t* __restrict__ dout, int
 
 // The first `readers` workgroups compute dprobs, the others dy: memory then
 // sees mostly reads and, behind them, mostly writes, which is faster than both
-// at once although dout is read twice (32768 tokens, top-8, 2048 wide: 373
+// at once although dout is read twice (32768 tokens, top-8, 2048 wide: 371
 // against 429 us, where dprobs alone takes 171 and dy alone 207; from 900 tokens
-// of 256 up it never lost). Bound by HBM: 2.42 GB in 373 us, 6.5 TB/s counting dout twice.
+// of 256 up it never lost). Bound by HBM: 2.42 GB in 371 us, 6.5 TB/s counting dout twice.
 template <bool F16, int LPR, int C>
 __global__ __launch_bounds__(kBwdThreads) void unpermute_bwd_kernel(
     const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y, int64_t p_end,

@@ -461,10 +461,11 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& p, const NsTile& tl, l
 // and the loads of stage s + NS are issued into the buffer just released.
 // W = 64, NS = 4 and W = 128, NS = 2 take 64 KiB of LDS, two workgroups per CU;
 // W = 128, NS = 4 is for launches of at most one workgroup per CU, which has
-// nobody to hide its loads' latency. The 128 x 128 tiles are bound by LDS
-// bandwidth (96 KiB per stage, 768 cycles against 512 of MFMA), the 64 x 64
-// ones by the CU's load path (16 KiB per stage, about 450 cycles against 128 of
-// MFMA) and, in short contractions, by their start and end (4500 cycles).
+// nobody to hide its loads' latency. The 128 x 128 tiles move 96 KiB through LDS
+// per stage, 768 cycles at 128 bytes each against 512 of MFMA (the square of
+// 16 x 1536: MFMA pipes busy 34% of the launch, CUs with work 81%); the 64 x 64
+// ones are bound by the CU's load path (16 KiB per stage, about 450 cycles against
+// 128 of MFMA) and, in short contractions, by their start and end (4500 cycles).
 // Each MFMA takes the second operand's fragment first, so a lane ends with
 // four consecutive columns of one row.
 template <int W, int NS, int MODE>
@@ -738,14 +739,14 @@ __global__ __launch_bounds__(TileW::NT, 1) void ns_gemm256_kernel(NsArgs p) {
 
 // A small matrix (rp <= 128 and at most 64 Ki padded elements) is iterated by
 // one workgroup in one launch: launches, not work, are what the general path
-// costs there (17 of them, 60 us for 64 x 256).
+// costs there (17 of them, 56 us for 64 x 256).
 //
 // 8 waves. Y's high half lives in LDS (up to 128 KiB) as rows of rp values;
 // wave w owns 16-row blocks w * RB .. + RB - 1 and holds their values in fp32 in
 // registers, in the accumulator layout: the product Y Q is added onto a Y held
 // there, so no low half is needed, and a wave's update touches its own rows
 // only. A (less mu I) and Q take turns in one (rp, rp) LDS array. 64 x 256 takes
-// 16 us (65 as 17 launches): 35 k cycles, of them 8 k until the first product,
+// 16 us: 35 k cycles, of them 8 k until the first product,
 // 2100 a step for the Gram product (LDS bandwidth) and 2100 for the update;
 // 64 x 1000 takes 54 us and 128 x 512 67 us.
 constexpr int kTinyThreads = 512;
@@ -1018,12 +1019,12 @@ __global__ __launch_bounds__(kTinyThreads) void ns_tiny_kernel(TinyArgs p) {
 static int ns_widest(int64_t rp) { return rp <= 64 ? 64 : rp <= 128 ? 128 : 256; }
 
 // Width of a product's tiles, and p's tile counts for it: 256 where those give
-// every CU a tile (five steps of 16 x 2048 x 1536: 1.78 ms, with 128 at most
-// 2.02 ms), else 128 where those give every second CU one (one 2048 x 3584: 457 us;
-// asking for one on every CU 477 us, and for one on every third, 3 x 777 x 1001
-// goes from 185 to 227 us), else 64. The square stays at 128: its K is the short
-// side, and two workgroups per CU hide more of its epilogue (16 x 2048 x 1536 1766
-// against 1805 us; for the Gram product it makes no difference).
+// every CU a tile (five steps of 16 x 2048 x 1536: 1774 us, with 128 at most
+// 2025), else 128 where those give every second CU one (one 2048 x 3584: 440 us,
+// asking for one on every CU 512; asking for one on every third, 16 x 300 x 2000
+// goes from 198 to 263 us), else 64. The square stays at 128: its K is the short
+// side, and two workgroups per CU hide more of its epilogue (16 x 2048 x 1536:
+// 1845 us with 256, 300 x 130 x 190: 454 against 385).
 template <int MODE>
 static int ns_plan(NsArgs& p, int64_t batch) {
   constexpr bool SYM = MODE == kGram || MODE == kSquare;
