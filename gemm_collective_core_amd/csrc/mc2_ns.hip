@@ -21,7 +21,7 @@
 // steps, and reached 1.5e-1 of the result. So Y is held as hi + lo, two fp16 (lo
 // times 2^11 more): the products use hi,
 //   Y' = hi Q~ + a lo,  Q~ = a I + b A + c A A,
-// and errors are 6e-4 to 2.5e-3 whatever the rank, where roundings average out;
+// and errors are 4e-4 to 2.7e-3 whatever the rank, where roundings average out;
 // few or equal singular values make them systematic (9e-3 for I, up to 3.5e-2).
 // The last step leaves lo out, since what it loses is not multiplied again.
 #include "../../include/mc2_train.h"

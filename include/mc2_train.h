@@ -103,17 +103,17 @@ int mc2_moe_permute_backward(const void* dpermuted, int64_t rows, const int32_t*
  * directions whose singular value is near zero is not multiplied by a in every
  * step. With the usual five steps of (3.4445, -4.7750, 2.0315), and before the
  * rounding to out_dtype, the error of the result (2-norm of the difference over
- * that of the result) is 6e-4 to 2.5e-3 where G has many different singular
- * values, zeros among them (gradients of any rank). It is larger where few or
- * equal singular values carry the matrix, since operand roundings do not
- * average out there and a step magnifies a relative error by up to 5: 9e-3 for
- * identity matrices, and 3.5e-2 at most over the spectra tried (2 or 3 nonzero
- * singular values). More steps magnify it further. |G|_F below 1e-5 eps leaves
- * iterates too small for fp16. Iterates are held in
- * range as long as their entries stay below 16 and the entries of A and
- * b A + c A A below 128 (coefficients whose iterates stay bounded, as those
- * do); beyond, the result is infinite or NaN. A NaN or infinity in G spreads
- * over its own matrix only. The same arguments give the same bits.
+ * that of the result) is 4e-4 to 2.7e-3 for dense matrices of any rank whose
+ * singular values differ, r >= 20 (gradients). It is larger where few or equal
+ * ones carry the matrix and operand roundings do not average out, since a
+ * step magnifies a relative error by up to 5: 9e-3 for identity matrices, and
+ * 3.5e-2 at most over the spectra tried (2 or 3 nonzero singular values). More
+ * steps magnify it further. |G|_F below 1e-5 eps leaves iterates too small for
+ * fp16. Iterates are held in range as long as their entries stay below 16 and
+ * the entries of A and b A + c A A below 128 (coefficients whose iterates stay
+ * bounded, as those do); beyond, the result is infinite or NaN. A NaN or
+ * infinity in G spreads over its own matrix only. The same arguments give the
+ * same bits.
  */
 size_t mc2_ns_workspace_size(int64_t batch, int64_t m, int64_t n);
 
