@@ -1,5 +1,5 @@
-"""Loads ``libmc2.so`` and declares the C ABI of ``include/mc2.h`` and
-``include/mc2_train.h``."""
+"""Loads ``libmc2.so`` and declares the C ABI of ``include/mc2.h``,
+``include/mc2_train.h`` and ``include/mc2_serve.h``."""
 from __future__ import annotations
 
 import ctypes as C
@@ -52,6 +52,18 @@ TRAIN_SIGNATURES = {
                                   _P, C.c_size_t, _P]),
 }
 
+# Entry points of include/mc2_serve.h
+SERVE_SIGNATURES = {
+    "mc2_mx4_row_bytes": (C.c_size_t, [_I64]),
+    "mc2_mx4_scale_bytes": (C.c_size_t, [_I64]),
+    "mc2_mx4_quantize": (_I, [_P, _I64, _I64, _I64, _I, _I, _P, _P, _P]),
+    "mc2_mx4_dequantize": (_I, [_P, _P, _I64, _I64, _I64, _I, _I, _P, _P]),
+    "mc2_mx4_mm_rs_local": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P, _I, _P, _P, _P,
+                                 _U32, _I, _P]),
+    "mc2_mx4_ag_mm_local": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P, _I, _P, _P, _P,
+                                 _U32, _I, _P]),
+}
+
 _lib = None
 
 
@@ -63,7 +75,8 @@ def load() -> C.CDLL:
             raise RuntimeError(
                 f"{LIB_PATH} is missing: build it with `python -m gemm_collective_core_amd.build`")
         lib = C.CDLL(LIB_PATH)
-        for name, (res, args) in {**SIGNATURES, **TRAIN_SIGNATURES}.items():
+        for name, (res, args) in {**SIGNATURES, **TRAIN_SIGNATURES,
+                                    **SERVE_SIGNATURES}.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args

@@ -1,4 +1,5 @@
-"""Thin Python binding over the C ABI of ``include/mc2.h`` and ``include/mc2_train.h``.
+"""Thin Python binding over the C ABI of ``include/mc2.h``, ``include/mc2_train.h``
+and ``include/mc2_serve.h``.
 
 Every function has the name of the C entry point it calls and only marshals
 arguments: it checks that tensors live on the GPU with the expected dtype and
@@ -638,3 +639,113 @@ def mc2_ns_orthogonalize(g, *, steps=5, coeffs=MC2_NS_COEFFS, eps=1e-7, scale=1.
                out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(dev))
     _check("mc2_ns_orthogonalize", st)
     return out
+
+
+_MX4_TYPES = (torch.bfloat16, torch.float16, torch.float32)
+
+
+def mc2_mx4_row_bytes(k) -> int:
+    """Bytes of codes in an MX4 row of k values."""
+    return int(_lib.load().mc2_mx4_row_bytes(k))
+
+
+def mc2_mx4_scale_bytes(k) -> int:
+    """Bytes of scales in an MX4 row of k values."""
+    return int(_lib.load().mc2_mx4_scale_bytes(k))
+
+
+def _want_mx4(codes, scales, name, shape, k, given=True):
+    """codes and scales hold the MX4 form of rows `shape` of k values (given:
+    neither may be None)."""
+    if given and (codes is None or scales is None):
+        raise ValueError(f"{name} needs codes and scales")
+    _want(codes, name, shape=(*shape, mc2_mx4_row_bytes(k)), dtype=torch.uint8)
+    _want(scales, name + "_scale", shape=(*shape, mc2_mx4_scale_bytes(k)), dtype=torch.uint8)
+
+
+def mc2_mx4_quantize(x, *, trans=False, codes=None, scales=None):
+    """MX4 form of x, (rows, k) or a stack (batch, rows, k) of bf16, fp16 or fp32,
+    or with trans (k, rows): returns (codes, scales), (..., rows, bytes) uint8,
+    with blocks of 32 along k."""
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be a matrix or a stack of matrices")
+    _want(x, "x", dtypes=_MX4_TYPES)
+    k, rows = (x.shape[-2], x.shape[-1]) if trans else (x.shape[-1], x.shape[-2])
+    lead = x.shape[:-2]
+    _want_mx4(codes, scales, "codes", (*lead, rows), k, given=False)
+    dev = _dev(x, codes, scales)
+    if codes is None:
+        codes = torch.empty((*lead, rows, mc2_mx4_row_bytes(k)), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((*lead, rows, mc2_mx4_scale_bytes(k)), dtype=torch.uint8, device=dev)
+    batch = 1 if x.dim() == 2 else x.shape[0]
+    st = _call(dev, _lib.load().mc2_mx4_quantize, x.data_ptr(), batch, rows, k, int(bool(trans)),
+               _CODES[x.dtype], codes.data_ptr(), scales.data_ptr(), _stream(dev))
+    _check("mc2_mx4_quantize", st)
+    return codes, scales
+
+
+def mc2_mx4_dequantize(codes, scales, k, *, trans=False, out_dtype=torch.bfloat16, out=None):
+    """The values of (..., rows, k), or with trans (..., k, rows), that codes and
+    scales stand for, in out_dtype (bf16, fp16 or fp32)."""
+    if codes.dim() not in (2, 3):
+        raise ValueError("codes must be (rows, bytes) or a stack of them")
+    lead, rows = codes.shape[:-2], codes.shape[-2]
+    _want_mx4(codes, scales, "codes", (*lead, rows), k)
+    shape = (*lead, k, rows) if trans else (*lead, rows, k)
+    out_dtype = out_dtype if out is None else out.dtype
+    if out_dtype not in _MX4_TYPES:
+        raise ValueError(f"out_dtype must be one of {_MX4_TYPES}, got {out_dtype}")
+    _want(out, "out", shape=shape)
+    dev = _dev(codes, scales, out)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    batch = 1 if codes.dim() == 2 else codes.shape[0]
+    st = _call(dev, _lib.load().mc2_mx4_dequantize, codes.data_ptr(), scales.data_ptr(), batch,
+               rows, k, int(bool(trans)), _CODES[out_dtype], out.data_ptr(), _stream(dev))
+    _check("mc2_mx4_dequantize", st)
+    return out
+
+
+def _mx4_mm(name, gather, x1, x1_scale, x2, x2_scale, k, world_size, rank, bias, out_dtype, out,
+            ready_flags, flag_counters, epoch, comm_turn):
+    if x1.dim() != 2 or x2.dim() != 2:
+        raise ValueError("x1 and x2 must hold the codes of matrices")
+    m, n = x1.shape[0], x2.shape[0]
+    _want_mx4(x1, x1_scale, "x1", (m,), k)
+    _want_mx4(x2, x2_scale, "x2", (n,), k)
+    if gather and (world_size < 1 or m % world_size):
+        raise ValueError("rows of x1 must be world_size * m_c")
+    _want(bias, "bias", shape=(n,), dtype=torch.bfloat16)
+    out_dtype = out_dtype if out is None else out.dtype
+    if out_dtype not in _MX4_TYPES:
+        raise ValueError(f"out_dtype must be one of {_MX4_TYPES}, got {out_dtype}")
+    _want(out, "out", shape=(m, n))
+    dev = _dev(x1, x1_scale, x2, x2_scale, bias, out, flag_counters)
+    _check_flags(world_size, comm_turn, ready_flags, flag_counters)
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+    st = _call(dev, getattr(_lib.load(), name), x1.data_ptr(), x1_scale.data_ptr(), x2.data_ptr(),
+               x2_scale.data_ptr(), m // world_size if gather else m, k, n, world_size, rank,
+               _ptr(bias), _CODES[out_dtype], out.data_ptr(), _ptr(ready_flags),
+               _ptr(flag_counters), epoch, comm_turn, _stream(dev))
+    _check(name, st)
+    return out
+
+
+def mc2_mx4_mm_rs_local(x1, x1_scale, x2, x2_scale, k, world_size, rank, *, bias=None,
+                        out_dtype=torch.bfloat16, out=None, ready_flags=None, flag_counters=None,
+                        epoch=0, comm_turn=0):
+    """MatmulReduceScatter compute share of two MX4 operands: x1 (m, k) @ x2
+    (n, k)^T + bias, each given as codes and scales. Returns out (m, n)."""
+    return _mx4_mm("mc2_mx4_mm_rs_local", False, x1, x1_scale, x2, x2_scale, k, world_size, rank,
+                   bias, out_dtype, out, ready_flags, flag_counters, epoch, comm_turn)
+
+
+def mc2_mx4_ag_mm_local(x_gathered, x_scale, x2, x2_scale, k, world_size, rank, *, bias=None,
+                        out_dtype=torch.bfloat16, out=None, ready_flags=None, flag_counters=None,
+                        epoch=0, comm_turn=0):
+    """AllGatherMatmul compute share of two MX4 operands: x_gathered (W * m_c, k)
+    @ x2 (n, k)^T + bias. Returns out."""
+    return _mx4_mm("mc2_mx4_ag_mm_local", True, x_gathered, x_scale, x2, x2_scale, k, world_size,
+                   rank, bias, out_dtype, out, ready_flags, flag_counters, epoch, comm_turn)

@@ -450,4 +450,7 @@ const char* mc2_version(void);
 /* The training-step operators around the grouped experts, from the same library. */
 #include "mc2_train.h"
 
+/* 4-bit operands and the MoE layer for few tokens, from the same library. */
+#include "mc2_serve.h"
+
 #endif /* MC2_H_ */
