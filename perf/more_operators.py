@@ -199,7 +199,7 @@ def _run_own(s):
     if s["weights"] == "bf16":
         return mc2.mc2_moe_tokens(s["x"], s["sel"], s["probs"], s["w1"], s["w2"], **kw)
     return mc2.mc2_moe_tokens(s["x"], s["sel"], s["probs"], s["w1"][0], s["w2"][0],
-                              w1_scale=s["w1"][1], w2_scale=s["w2"][1], inter=s["I"], **kw)
+                              w1_scale=s["w1"][1], w2_scale=s["w2"][1], **kw)
 
 
 def run(s):
