@@ -62,6 +62,9 @@ SERVE_SIGNATURES = {
                                  _U32, _I, _P]),
     "mc2_mx4_ag_mm_local": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P, _I, _P, _P, _P,
                                  _U32, _I, _P]),
+    "mc2_moe_tokens_workspace_size": (C.c_size_t, [_I64, _I, _I64, _I64]),
+    "mc2_moe_tokens": (_I, [_P, _P, _P, _I64, _I, _I64, _I, _I, _I, _I, _P, _P, _P, _P, _I64, _P,
+                            _P, C.c_size_t, _P, _P]),
 }
 
 _lib = None

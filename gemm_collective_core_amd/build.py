@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmc2.so")
 SOURCES = ["mc2_gemm.hip", "mc2_allreduce.hip", "mc2_grouped.hip", "mc2_moe.hip",
-           "mc2_moe_bwd.hip", "mc2_ns.hip", "mc2_mx4.hip", "mc2_mx4_gemm.hip"]
+           "mc2_moe_bwd.hip", "mc2_ns.hip", "mc2_mx4.hip", "mc2_mx4_gemm.hip",
+           "mc2_moe_tokens.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -1,0 +1,602 @@
+// A whole MoE layer for few tokens (mc2_moe_tokens), for gfx950: two launches.
+//
+// Decoding reads every named expert's weights for a handful of rows, so the
+// weights' bytes bound it: 75 MB for one token, top-8, of the layer with 2048 x
+// 1536 and 768 x 2048 bf16 experts. Both kernels stream them once, straight from
+// memory into the registers that the matrix instructions take them from:
+//
+//   tokens_fc1_kernel: a workgroup computes a strip of gate columns and the same
+//     strip of up columns for all the rows of one expert, each wave over a part
+//     of H; the waves' sums meet in LDS, SwiGLU follows, and h leaves as the sum
+//     of two bf16 numbers.
+//   tokens_fc2_kernel: the same with h and w2 for a strip of output columns. The
+//     results y of a slot stay fp32 in the workspace; the workgroup that is the
+//     last of its strip adds them up per token, in slot order, with the weights.
+//
+// A workgroup finds its expert by itself: the a-th expert, in order of id, that a
+// slot names, and that expert's slots (no sorting launch, no count on the
+// host). Rows of the 16-row operand that no slot fills repeat the last one and
+// are dropped: rows of a product do not mix, so neither do their NaN.
+#include "mc2_mx4.hpp"
+#include "mc2_tiles.hpp"
+
+namespace mc2 {
+
+constexpr int kTokMaxSlots = 4096;   // T * K
+constexpr int kTokMaxExperts = 1024;
+constexpr int kCpolAgent = 0x10;     // sc1: coherent over the XCDs' L2s
+
+// Strips of fc2 at most: 16 columns each.
+__host__ __device__ constexpr int64_t tok_strips(int64_t H) { return (H + 15) / 16; }
+
+struct TokArgs {
+  const uint16_t* x;
+  const int32_t* sel;
+  const float* probs;
+  const char* w1;
+  const char* w1s;
+  const char* w2;
+  const char* w2s;
+  uint16_t* out;
+  uint32_t* arrived;  // per strip of fc2
+  uint16_t* h_hi;
+  uint16_t* h_lo;
+  float* y;
+  int32_t* dev_err;
+  int64_t H, I;
+  int T, K, TK, E, e0, El;
+};
+
+// Which expert (of this rank's) a workgroup works for, its slots, and how many
+// experts are named at all.
+struct Expert {
+  int e, count, named;
+};
+
+template <int NT>
+struct PickMem {
+  uint32_t words[kTokMaxExperts / 32];
+  int count;
+  uint16_t list[kTokMaxSlots];
+};
+
+// Expert number `a` of those named, in order of id (e = -1 past the last), and
+// its slots in mem.list, in any order: rows of a product do not mix.
+template <int NT>
+__device__ __forceinline__ Expert pick_expert(const TokArgs& p, int a, PickMem<NT>& mem) {
+  constexpr int PER = kTokMaxSlots / NT;
+  const int lane = threadIdx.x & 63;
+  if (threadIdx.x < kTokMaxExperts / 32) mem.words[threadIdx.x] = 0;
+  if (threadIdx.x == 0) mem.count = 0;
+  int id[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int s = threadIdx.x + i * NT;
+    id[i] = -1;
+    if (i * NT < p.TK && s < p.TK) {
+      const int e = p.sel[s] - p.e0;
+      id[i] = e >= 0 && e < p.El ? e : -1;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (id[i] >= 0) atomicOr(&mem.words[id[i] >> 5], 1u << (id[i] & 31));
+  __syncthreads();
+  // every wave: lanes hold the words, their running count of bits
+  const uint32_t w = lane < kTokMaxExperts / 32 ? mem.words[lane] : 0u;
+  int sum = __popc(w);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up(sum, d);
+    if (lane >= d && lane < 32) sum += o;
+  }
+  Expert r;
+  r.named = __builtin_amdgcn_readlane(sum, 31);
+  r.e = -1;
+  r.count = 0;
+  if (a >= r.named) return r;  // uniform over the workgroup
+  const int before = sum - __popc(w);
+  const uint64_t mine = __ballot(lane < 32 && before <= a && a < sum);
+  const int wl = __builtin_ctzll(mine);
+  uint32_t bits = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w), wl));
+  for (int skip = a - __builtin_amdgcn_readlane(before, wl); skip > 0; --skip) bits &= bits - 1;
+  r.e = __builtin_amdgcn_readfirstlane(wl * 32 + __builtin_ctz(bits));
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (id[i] == r.e) mem.list[atomicAdd(&mem.count, 1)] = static_cast<uint16_t>(threadIdx.x + i * NT);
+  __syncthreads();
+  r.count = __builtin_amdgcn_readfirstlane(mem.count);
+  return r;
+}
+
+// ------------------------------------------------------------------- weights
+//
+// A step of K for a strip of 16 * NF columns of one matrix: load() brings this
+// lane's part into registers, frag<T>(f) is the operand of fragment f (16
+// columns) for sub-step T of KT, 32 K values each. k0(s, T, g): first of the
+// eight K values that lane group g holds of it. Column c of the strip is lane
+// lane_of(c) & 15 of fragment frag_of(c).
+
+// bf16 weights (rows of K, columns contiguous): a lane loads LC neighbouring
+// columns of eight K rows; the eight values of a column then lie in one lane
+// and a byte permute pairs them up, so that the strip's columns go to fragments
+// by their place among the LC: fragment f holds columns LC * n + f.
+template <int LC_>
+struct WBf16 {
+  static constexpr int NF = LC_, LC = LC_, KS = 32, KT = 1, NW = 8;
+  static constexpr int U = LC_ == 2 ? 4 : 2;  // steps in flight
+  uint32_t r[8][LC_ / 2];
+
+  struct Strip {
+    const char* base;  // column 0 of the strip in K row 0
+    uint32_t off;      // this lane's columns in K row 8 g
+    uint32_t ld;       // bytes between K rows
+    int64_t k;
+  };
+  static __device__ __forceinline__ Strip strip(const char* w, const char*, int64_t e, int64_t K,
+                                                int64_t cols, int64_t first, int64_t c0,
+                                                int64_t limit) {
+    const int lane = threadIdx.x & 63;
+    const int64_t mine = LC * (lane & 15), most = limit - LC - c0;
+    return {w + (e * K * cols + first + c0) * 2,
+            static_cast<uint32_t>((8 * (lane >> 4) * cols + (mine < most ? mine : most)) * 2),
+            static_cast<uint32_t>(cols * 2), K};
+  }
+  // (32-bit offsets from a scalar base: 64-bit addresses would take two
+  // registers for each load in flight)
+  __device__ __forceinline__ void load(const Strip& st, int64_t s) {
+    const int64_t row = s * 32 + 8 * ((threadIdx.x & 63) >> 4);
+    // k is a multiple of 8: all eight rows or none
+    const uint32_t off = row < st.k ? st.off : kOffNone;
+    const __amdgpu_buffer_rsrc_t q = make_rsrc(st.base + s * 32 * st.ld);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (LC == 4) {
+        const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(q, off, i * st.ld, 0);
+        r[i][0] = v[0];
+        r[i][1] = v[1];
+      } else {
+        r[i][0] = __builtin_amdgcn_raw_buffer_load_b32(q, off, i * st.ld, 0);
+      }
+    }
+  }
+  template <int T>
+  __device__ __forceinline__ bf16x8_t frag(int f) const {
+    u32x4_t v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = __builtin_amdgcn_perm(r[2 * i + 1][f >> 1], r[2 * i][f >> 1],
+                                   (f & 1) ? 0x07060302u : 0x05040100u);
+    return bit_cast<bf16x8_t>(v);
+  }
+  static __device__ __forceinline__ int64_t k0(int64_t s, int, int g) { return s * 32 + 8 * g; }
+  static __device__ __forceinline__ int frag_of(int c) { return c % LC; }
+  static __device__ __forceinline__ int lane_of(int c) { return c / LC; }
+};
+
+// MX4 weights (a row per column, K contiguous): a lane holds a block of 32 K
+// values of each of its NF columns, 16 n + the fragment's first, and turns eight
+// of them at a time into exact bf16 numbers.
+template <int NF_>
+struct WMx4 {
+  static constexpr int NF = NF_, KS = 128, KT = 4, NW = 4;
+  static constexpr int U = 2;
+  u32x4_t c[NF_];
+  float s[NF_];
+
+  struct Strip {
+    const char* base;
+    const char* sbase;
+    uint32_t off[NF_], soff[NF_];  // this lane's column and block g
+    int64_t nb;
+  };
+  static __device__ __forceinline__ Strip strip(const char* w, const char* ws, int64_t e, int64_t K,
+                                                int64_t cols, int64_t first, int64_t c0,
+                                                int64_t limit) {
+    const int lane = threadIdx.x & 63;
+    Strip st;
+    st.nb = (K + 31) / 32;
+    const int64_t pitch = (st.nb + 15) / 16 * 16, row0 = e * cols + first + c0;
+    st.base = w + row0 * st.nb * 16;
+    st.sbase = ws + row0 * pitch;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const int64_t mine = 16 * f + (lane & 15), most = limit - 1 - c0;
+      const int64_t c = mine < most ? mine : most;
+      st.off[f] = static_cast<uint32_t>((c * st.nb + (lane >> 4)) * 16);
+      st.soff[f] = static_cast<uint32_t>(c * pitch + (lane >> 4));
+    }
+    return st;
+  }
+  __device__ __forceinline__ void load(const Strip& st, int64_t step) {
+    const bool in = step * 4 + ((threadIdx.x & 63) >> 4) < st.nb;
+    const __amdgpu_buffer_rsrc_t q = make_rsrc(st.base + step * 64);
+    const __amdgpu_buffer_rsrc_t qs = make_rsrc(st.sbase + step * 4);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      c[f] = __builtin_amdgcn_raw_buffer_load_b128(q, in ? st.off[f] : kOffNone, 0, 0);
+      s[f] = mx4_scale(__builtin_amdgcn_raw_buffer_load_b8(qs, in ? st.soff[f] : kOffNone, 0, 0));
+    }
+  }
+  template <int T>
+  __device__ __forceinline__ bf16x8_t frag(int f) const {
+    return bit_cast<bf16x8_t>(mx4_bf16x8(c[f][T], s[f]));
+  }
+  static __device__ __forceinline__ int64_t k0(int64_t s, int t, int g) {
+    return s * 128 + 32 * g + 8 * t;
+  }
+  static __device__ __forceinline__ int frag_of(int c) { return c / 16; }
+  static __device__ __forceinline__ int lane_of(int c) { return c % 16; }
+};
+
+__device__ __forceinline__ f32x4_t mfma_bf16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// The waves' sums of NV values a lane (one 16-row tile), through LDS: element
+// (m, v, c) of the tile is red[w][v][(m >> 2) * 16 + n][m & 3] of every wave.
+template <int NW, int NV>
+__device__ __forceinline__ float tile_sum(const f32x4_t (&red)[NW][NV][64], int v, int m, int n) {
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) s += red[w][v][(m >> 2) * 16 + n][m & 3];
+  return s;
+}
+
+// ----------------------------------------------------------------------- fc1
+
+// h of up to 16 * MT slots, list[0 .. count), of the strip's columns.
+template <class W, int MT>
+__device__ __forceinline__ void fc1_rows(const TokArgs& p, const uint16_t* list, int count,
+                                         const typename W::Strip& sg, const typename W::Strip& su,
+                                         int64_t c0, f32x4_t (&red)[W::NW][2 * W::NF][64]) {
+  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U : 1;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(reinterpret_cast<const char*>(p.x));
+  uint32_t xr[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int r = 16 * i + (lane & 15);
+    xr[i] = static_cast<uint32_t>(list[r < count ? r : count - 1] / p.K * p.H * 2);
+  }
+  f32x4_t ag[NF][MT], au[NF][MT];
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ag[f][i] = au[f][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int64_t steps = (p.H + W::KS - 1) / W::KS;
+  for (int64_t s0 = wave; s0 < steps; s0 += NW * U) {
+    W wg[U], wu[U];
+    u32x4_t a[U][W::KT][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t s = s0 + u * NW;
+      wg[u].load(sg, s);
+      wu[u].load(su, s);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < W::KT; ++t) {
+        const int64_t k = W::k0(s0 + u * NW, t, g);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          a[u][t][i] = __builtin_amdgcn_raw_buffer_load_b128(
+              rx, k < p.H ? xr[i] + static_cast<uint32_t>(2 * k) : kOffNone, 0, 0);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      sfor<W::KT>([&](auto Tc) {
+        constexpr int t = decltype(Tc)::value;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          const bf16x8_t bg = wg[u].template frag<t>(f), bu = wu[u].template frag<t>(f);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            ag[f][i] = mfma_bf16(bit_cast<bf16x8_t>(a[u][t][i]), bg, ag[f][i]);
+            au[f][i] = mfma_bf16(bit_cast<bf16x8_t>(a[u][t][i]), bu, au[f][i]);
+          }
+        }
+      });
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    if (i) __syncthreads();
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      red[wave][f][lane] = ag[f][i];
+      red[wave][NF + f][lane] = au[f][i];
+    }
+    __syncthreads();
+    const int rows = count - 16 * i < 16 ? count - 16 * i : 16;
+    for (int q = threadIdx.x; q < rows * (16 * NF); q += NW * 64) {
+      const int m = q / (16 * NF), c = q - m * (16 * NF);
+      const int f = W::frag_of(c), n = W::lane_of(c);
+      if (c0 + c >= p.I) continue;
+      const float gate = tile_sum<NW>(red, f, m, n), up = tile_sum<NW>(red, NF + f, m, n);
+      const float h = gate / (1.f + __expf(-gate)) * up;
+      const uint16_t hi = f32_to_bf16_bits(h);
+      const float hf = bf16_bits_to_f32(hi);
+      // (an infinite h has no rest)
+      const float lo = __builtin_fabsf(hf) < __builtin_inff() ? h - hf : 0.f;
+      const int64_t at = static_cast<int64_t>(list[16 * i + m]) * p.I + c0 + c;
+      p.h_hi[at] = hi;
+      p.h_lo[at] = f32_to_bf16_bits(lo);
+    }
+  }
+  __syncthreads();
+}
+
+// MANY: more than 16 tokens, so that an expert may have more than 16 slots
+// of different tokens; they are then taken 64 at a time.
+template <class W, bool MANY>
+__global__ __launch_bounds__(W::NW * 64) void tokens_fc1_kernel(TokArgs p) {
+  constexpr int NT = W::NW * 64;
+  __shared__ PickMem<NT> mem;
+  __shared__ f32x4_t red[W::NW][2 * W::NF][64];
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    for (int64_t i = threadIdx.x; i < tok_strips(p.H); i += NT) p.arrived[i] = 0;
+    for (int s = threadIdx.x; s < p.TK; s += NT)
+      if (p.sel[s] < 0 || p.sel[s] >= p.E) atomic_or_err(p.dev_err, MC2_DEVERR_EXPERT_ID);
+  }
+  const Expert ex = pick_expert<NT>(p, blockIdx.y, mem);
+  if (ex.e < 0) return;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * (16 * W::NF);
+  const auto sg = W::strip(p.w1, p.w1s, ex.e, p.H, 2 * p.I, 0, c0, p.I);
+  const auto su = W::strip(p.w1, p.w1s, ex.e, p.H, 2 * p.I, p.I, c0, p.I);
+  for (int b = 0; b < ex.count;) {
+    const int left = ex.count - b;
+    if (MANY && left > 16) {
+      fc1_rows<W, 4>(p, mem.list + b, left < 64 ? left : 64, sg, su, c0, red);
+      b += 64;
+    } else {
+      fc1_rows<W, 1>(p, mem.list + b, left < 16 ? left : 16, sg, su, c0, red);
+      b += 16;
+    }
+  }
+}
+
+// ----------------------------------------------------------------------- fc2
+
+template <class W, int MT>
+__device__ __forceinline__ void fc2_rows(const TokArgs& p, const uint16_t* list, int count,
+                                         const typename W::Strip& sw, int64_t c0,
+                                         f32x4_t (&red)[W::NW][W::NF][64]) {
+  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U : 1;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const __amdgpu_buffer_rsrc_t rhi = make_rsrc(reinterpret_cast<const char*>(p.h_hi));
+  const __amdgpu_buffer_rsrc_t rlo = make_rsrc(reinterpret_cast<const char*>(p.h_lo));
+  uint32_t hr[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int r = 16 * i + (lane & 15);
+    hr[i] = static_cast<uint32_t>(list[r < count ? r : count - 1] * p.I * 2);
+  }
+  f32x4_t acc[NF][MT];
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[f][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int64_t steps = (p.I + W::KS - 1) / W::KS;
+  for (int64_t s0 = wave; s0 < steps; s0 += NW * U) {
+    W w[U];
+    u32x4_t hi[U][W::KT][MT], lo[U][W::KT][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u].load(sw, s0 + u * NW);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < W::KT; ++t) {
+        const int64_t k = W::k0(s0 + u * NW, t, g);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const uint32_t off = k < p.I ? hr[i] + static_cast<uint32_t>(2 * k) : kOffNone;
+          hi[u][t][i] = __builtin_amdgcn_raw_buffer_load_b128(rhi, off, 0, 0);
+          lo[u][t][i] = __builtin_amdgcn_raw_buffer_load_b128(rlo, off, 0, 0);
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      sfor<W::KT>([&](auto Tc) {
+        constexpr int t = decltype(Tc)::value;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          const bf16x8_t b = w[u].template frag<t>(f);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(hi[u][t][i]), b, acc[f][i]);
+            acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(lo[u][t][i]), b, acc[f][i]);
+          }
+        }
+      });
+  }
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(reinterpret_cast<const char*>(p.y));
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    if (i) __syncthreads();
+#pragma unroll
+    for (int f = 0; f < NF; ++f) red[wave][f][lane] = acc[f][i];
+    __syncthreads();
+    const int rows = count - 16 * i < 16 ? count - 16 * i : 16;
+    for (int q = threadIdx.x; q < rows * (16 * NF); q += NW * 64) {
+      const int m = q / (16 * NF), c = q - m * (16 * NF);
+      if (c0 + c >= p.H) continue;
+      const float v = tile_sum<NW>(red, W::frag_of(c), m, W::lane_of(c));
+      const int64_t at = static_cast<int64_t>(list[16 * i + m]) * p.H + c0 + c;
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ry, static_cast<int>(at * 4), 0,
+                                            kCpolAgent);
+    }
+  }
+  __syncthreads();
+}
+
+// out[t] = sum over the local slots of t, in slot order, of probs * y: columns
+// c0 .. c0 + cw of every token.
+template <int NT>
+__device__ __forceinline__ void sum_slots(const TokArgs& p, int64_t c0, int cw) {
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(reinterpret_cast<const char*>(p.y));
+  const int q4 = cw / 4;
+  for (int q = threadIdx.x; q < p.T * q4; q += NT) {
+    const int t = q / q4;
+    const int64_t c = c0 + 4 * (q - t * q4);
+    if (c >= p.H) continue;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < p.K; ++k) {
+      const int s = t * p.K + k, e = p.sel[s] - p.e0;
+      if (e < 0 || e >= p.El) continue;
+      const float w = p.probs[s];
+      const u32x4_t y = __builtin_amdgcn_raw_buffer_load_b128(
+          ry, static_cast<int>((static_cast<int64_t>(s) * p.H + c) * 4), 0, kCpolAgent);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(w, __uint_as_float(y[j]), v[j]);
+    }
+    *reinterpret_cast<u32x2_t*>(p.out + static_cast<int64_t>(t) * p.H + c) = pack4<Out::BF16>(v);
+  }
+}
+
+template <class W, bool MANY>
+__global__ __launch_bounds__(W::NW * 64) void tokens_fc2_kernel(TokArgs p) {
+  constexpr int NT = W::NW * 64, CW = 16 * W::NF;
+  __shared__ PickMem<NT> mem;
+  __shared__ f32x4_t red[W::NW][W::NF][64];
+  __shared__ int last;
+  const Expert ex = pick_expert<NT>(p, blockIdx.y, mem);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * CW;
+  if (ex.e < 0) {
+    // no slot is local: the output is zeros
+    if (ex.named == 0 && blockIdx.y == 0) sum_slots<NT>(p, c0, CW);
+    return;
+  }
+  const auto sw = W::strip(p.w2, p.w2s, ex.e, p.I, p.H, 0, c0, p.H);
+  for (int b = 0; b < ex.count;) {
+    const int left = ex.count - b;
+    if (MANY && left > 16) {
+      fc2_rows<W, 4>(p, mem.list + b, left < 64 ? left : 64, sw, c0, red);
+      b += 64;
+    } else {
+      fc2_rows<W, 1>(p, mem.list + b, left < 16 ? left : 16, sw, c0, red);
+      b += 16;
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    const uint32_t before = __hip_atomic_fetch_add(&p.arrived[blockIdx.x], 1u, __ATOMIC_RELAXED,
+                                                   __HIP_MEMORY_SCOPE_AGENT);
+    last = before + 1 == static_cast<uint32_t>(ex.named);
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  }
+  __syncthreads();
+  if (last) sum_slots<NT>(p, c0, CW);
+}
+
+// ------------------------------------------------------------------ host side
+
+struct TokWorkspace {
+  size_t arrived, h, y, bytes;
+};
+
+static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+static bool tok_workspace(int64_t T, int K, int64_t H, int64_t I, TokWorkspace& w) {
+  if (T < 1 || T > 256 || K < 1 || K > 64 || T * K > kTokMaxSlots) return false;
+  if (H < 8 || H > 65536 || I < 8 || I > 65536) return false;
+  const int64_t TK = T * K;
+  if (TK * H >= int64_t{1} << 28 || TK * I >= int64_t{1} << 28) return false;
+  w.arrived = 0;
+  w.h = up256(static_cast<size_t>(tok_strips(H)) * 4);
+  w.y = w.h + up256(static_cast<size_t>(TK * I) * 2) * 2;
+  w.bytes = w.y + up256(static_cast<size_t>(TK * H) * 4);
+  return true;
+}
+
+template <class W, bool MANY>
+static void launch_fc1(const TokArgs& a, int slots, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.I + 16 * W::NF - 1) / (16 * W::NF)), slots);
+  hipLaunchKernelGGL((tokens_fc1_kernel<W, MANY>), grid, dim3(W::NW * 64), 0, s, a);
+}
+template <class W, bool MANY>
+static void launch_fc2(const TokArgs& a, int slots, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.H + 16 * W::NF - 1) / (16 * W::NF)), slots);
+  hipLaunchKernelGGL((tokens_fc2_kernel<W, MANY>), grid, dim3(W::NW * 64), 0, s, a);
+}
+
+// Narrow strips where wide ones would not fill the CUs.
+template <bool MANY>
+static void launch_tokens(const TokArgs& a, bool mx4, hipStream_t s) {
+  const int slots = a.TK < a.El ? a.TK : a.El;
+  const int64_t cus = num_cus();
+  const bool wide1 = slots * ((a.I + 63) / 64) >= cus, wide2 = slots * ((a.H + 63) / 64) >= cus;
+  if (mx4) {
+    if (wide1) launch_fc1<WMx4<2>, MANY>(a, slots, s);
+    else launch_fc1<WMx4<1>, MANY>(a, slots, s);
+    if (wide2) launch_fc2<WMx4<2>, MANY>(a, slots, s);
+    else launch_fc2<WMx4<1>, MANY>(a, slots, s);
+  } else {
+    if (wide1) launch_fc1<WBf16<4>, MANY>(a, slots, s);
+    else launch_fc1<WBf16<2>, MANY>(a, slots, s);
+    if (wide2) launch_fc2<WBf16<4>, MANY>(a, slots, s);
+    else launch_fc2<WBf16<2>, MANY>(a, slots, s);
+  }
+}
+
+}  // namespace mc2
+
+using namespace mc2;
+
+extern "C" size_t mc2_moe_tokens_workspace_size(int64_t T, int K, int64_t H, int64_t I) {
+  TokWorkspace w;
+  return tok_workspace(T, K, H, I, w) ? w.bytes : 0;
+}
+
+extern "C" int mc2_moe_tokens(const void* x, const int32_t* sel, const float* probs, int64_t T,
+                              int K, int64_t H, int num_experts, int ep_rank, int local_experts,
+                              int w_dtype, const void* w1, const void* w1_scale, const void* w2,
+                              const void* w2_scale, int64_t I, void* out, void* workspace,
+                              size_t ws_bytes, int32_t* dev_err, hipStream_t stream) {
+  if (!x || !sel || !probs || !w1 || !w2 || !out || !workspace) return MC2_ERR_NULL;
+  if (w_dtype != MC2_BF16 && w_dtype != MC2_MX4) return MC2_ERR_DTYPE;
+  const bool mx4 = w_dtype == MC2_MX4;
+  if (mx4 && (!w1_scale || !w2_scale)) return MC2_ERR_NULL;
+  if (!mx4 && (w1_scale || w2_scale)) return MC2_ERR_DTYPE;
+  TokWorkspace w;
+  if (!tok_workspace(T, K, H, I, w)) return MC2_ERR_SHAPE;
+  if (num_experts < 1 || local_experts < 1 || local_experts > kTokMaxExperts || ep_rank < 0 ||
+      (static_cast<int64_t>(ep_rank) + 1) * local_experts > num_experts)
+    return MC2_ERR_SHAPE;
+  if (H % 8 || I % 8) return MC2_ERR_ALIGN;
+  if (!aligned16(x) || !aligned16(w1) || !aligned16(w2) || !aligned16(w1_scale) ||
+      !aligned16(w2_scale) || !aligned16(out) || !aligned16(workspace))
+    return MC2_ERR_ALIGN;
+  if (ws_bytes < w.bytes) return MC2_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  TokArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.sel = sel;
+  a.probs = probs;
+  a.w1 = static_cast<const char*>(w1);
+  a.w1s = static_cast<const char*>(w1_scale);
+  a.w2 = static_cast<const char*>(w2);
+  a.w2s = static_cast<const char*>(w2_scale);
+  a.out = static_cast<uint16_t*>(out);
+  a.arrived = reinterpret_cast<uint32_t*>(ws + w.arrived);
+  a.h_hi = reinterpret_cast<uint16_t*>(ws + w.h);
+  a.h_lo = reinterpret_cast<uint16_t*>(ws + w.h + (w.y - w.h) / 2);
+  a.y = reinterpret_cast<float*>(ws + w.y);
+  a.dev_err = dev_err;
+  a.H = H;
+  a.I = I;
+  a.T = static_cast<int>(T);
+  a.K = K;
+  a.TK = static_cast<int>(T) * K;
+  a.E = num_experts;
+  a.e0 = ep_rank * local_experts;
+  a.El = local_experts;
+  if (T > 16) launch_tokens<true>(a, mx4, stream);
+  else launch_tokens<false>(a, mx4, stream);
+  return hipGetLastError() == hipSuccess ? MC2_OK : MC2_ERR_HIP;
+}

@@ -749,3 +749,48 @@ def mc2_mx4_ag_mm_local(x_gathered, x_scale, x2, x2_scale, k, world_size, rank, 
     @ x2 (n, k)^T + bias. Returns out."""
     return _mx4_mm("mc2_mx4_ag_mm_local", True, x_gathered, x_scale, x2, x2_scale, k, world_size,
                    rank, bias, out_dtype, out, ready_flags, flag_counters, epoch, comm_turn)
+
+
+MC2_MX4 = 5
+
+
+def mc2_moe_tokens_workspace_size(T, K, H, I) -> int:
+    return int(_lib.load().mc2_moe_tokens_workspace_size(T, K, H, I))
+
+
+def mc2_moe_tokens(x, sel, probs, w1, w2, *, ep_rank, num_experts, w1_scale=None, w2_scale=None,
+                   out=None, workspace=None, dev_err=None):
+    """This rank's share of a whole MoE layer for few tokens: x (T, H) bf16, sel
+    (T, K) int32, probs (T, K) fp32. Weights in bf16, w1 (E_l, H, 2I) and w2
+    (E_l, I, H), or with w1_scale and w2_scale in MX4: mc2_mx4_quantize of
+    those with trans. Returns out (T, H)."""
+    if x.dim() != 2 or sel.dim() != 2 or probs.dim() != 2 or w1.dim() != 3 or w2.dim() != 3:
+        raise ValueError("x must be (T, H), sel and probs (T, K), w1 and w2 stacks of E_l")
+    (T, H), K, E_l = x.shape, sel.shape[1], w1.shape[0]
+    if (w1_scale is None) != (w2_scale is None):
+        raise ValueError("w1_scale and w2_scale go together")
+    mx4 = w1_scale is not None
+    if mx4:
+        I = w1.shape[1] // 2
+        _want_mx4(w1, w1_scale, "w1", (E_l, 2 * I), H)
+        _want_mx4(w2, w2_scale, "w2", (E_l, H), I)
+    else:
+        I = w2.shape[1]
+        _want(w1, "w1", shape=(E_l, H, 2 * I), dtype=torch.bfloat16)
+        _want(w2, "w2", shape=(E_l, I, H), dtype=torch.bfloat16)
+    _want(x, "x", dtype=torch.bfloat16)
+    _want(sel, "sel", shape=(T, K), dtype=torch.int32)
+    _want(probs, "probs", shape=(T, K), dtype=torch.float32)
+    _want(out, "out", shape=(T, H), dtype=torch.bfloat16)
+    _want(workspace, "workspace", dtype=torch.uint8)
+    _want(dev_err, "dev_err", **_ERR)
+    dev = _dev(x, sel, probs, w1, w2, w1_scale, w2_scale, out, workspace, dev_err)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    workspace = _workspace(mc2_moe_tokens_workspace_size(T, K, H, I), workspace, dev)
+    st = _call(dev, _lib.load().mc2_moe_tokens, x.data_ptr(), sel.data_ptr(), probs.data_ptr(), T,
+               K, H, num_experts, ep_rank, E_l, MC2_MX4 if mx4 else MC2_BF16, w1.data_ptr(),
+               _ptr(w1_scale), w2.data_ptr(), _ptr(w2_scale), I, out.data_ptr(),
+               workspace.data_ptr(), workspace.numel(), _ptr(dev_err), _stream(dev))
+    _check("mc2_moe_tokens", st)
+    return out

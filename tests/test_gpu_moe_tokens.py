@@ -1,0 +1,234 @@
+"""The MoE layer for few tokens against its oracle: exactly, on inputs whose
+every intermediate is a small integer, and on drawn ones; and the calls that
+decoding makes of it (captured, on another stream, one workspace after
+another)."""
+import numpy as np
+import pytest
+import torch
+
+from gemm_collective_core_amd import mc2
+from oracle import moe_tokens as ot
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def route(g, T, K, E, how):
+    if how == "one":  # every slot to one expert
+        return torch.full((T, K), E // 2, dtype=torch.int32)
+    if how == "dup":  # the same expert several times in a token
+        return torch.randint(0, E, (T, 1), generator=g, dtype=torch.int32).expand(T, K).contiguous()
+    if how == "bad":  # some ids out of range
+        s = torch.randint(0, E, (T, K), generator=g, dtype=torch.int32)
+        s.view(-1)[::3] = torch.tensor([-1, E, 2 ** 31 - 1, -2 ** 31, E + 5],
+                                       dtype=torch.int32).repeat(T * K)[:len(s.view(-1)[::3])]
+        return s
+    p = torch.rand((T, E), generator=g) + 0.5 * torch.rand((1, E), generator=g)
+    return p.topk(min(K, E), 1).indices.to(torch.int32) if K <= E else torch.randint(
+        0, E, (T, K), generator=g, dtype=torch.int32)
+
+
+def integer_case(T, H, I, E, E_l, K, how, seed):
+    """Column 0 of x is 192 and its gate weights +-1, all other x and w1 in {-1,
+    0, 1}: a gate is then beyond +-128, where silu is the identity or zero in
+    fp32 (exp(-128) < 2^-149), and h = gate * up is an integer of at most 16
+    bits, which two bf16 numbers hold. w2 in {-2 .. 2} and powers of two as
+    routing weights keep every sum exact in fp32."""
+    g = torch.Generator().manual_seed(seed)
+    small = lambda *s: torch.randint(-1, 2, s, generator=g).float()  # noqa: E731
+    x = small(T, H) * (torch.rand((T, H), generator=g) < min(1.0, 250 / H))
+    x[:, 0] = 192
+    w1 = small(E_l, H, 2 * I)
+    w1[:, 0, :I] = torch.where(torch.rand((E_l, I), generator=g) < 0.7, 1.0, -1.0)
+    w1[:, 0, I:] = 0
+    w2 = torch.randint(-2, 3, (E_l, I, H), generator=g).float()
+    probs = 2.0 ** torch.randint(-2, 2, (T, K), generator=g).float()
+    return x.to(BF), route(g, T, K, E, how), probs, w1.to(BF), w2.to(BF)
+
+
+def own(x, sel, probs, w1, w2, mx4, **kw):
+    x, sel, probs, w1, w2 = (t.cuda() for t in (x, sel, probs, w1, w2))
+    if mx4:
+        (w1, s1), (w2, s2) = (mc2.mc2_mx4_quantize(w, trans=True) for w in (w1, w2))
+        kw.update(w1_scale=s1, w2_scale=s2)
+    return mc2.mc2_moe_tokens(x, sel, probs, w1, w2, **kw)
+
+
+CASES = [
+    # T, H, I, E, E_l, K, routing
+    (1, 8, 8, 4, 4, 1, "top"), (1, 264, 136, 32, 32, 8, "top"), (2, 72, 40, 8, 8, 2, "top"),
+    (1, 136, 72, 8, 8, 4, "dup"), (16, 40, 264, 16, 16, 4, "top"), (16, 264, 72, 6, 3, 5, "one"),
+    (17, 136, 136, 8, 8, 2, "one"), (17, 264, 8, 60, 15, 4, "top"), (37, 1416, 200, 32, 8, 6, "top"),
+    (64, 264, 136, 128, 128, 8, "top"), (65, 72, 72, 5, 5, 1, "one"), (130, 136, 104, 3, 1, 3, "dup"),
+    (256, 72, 40, 16, 16, 16, "top"), (40, 200, 72, 16, 4, 4, "bad"), (3, 2056, 24, 1024, 512, 64, "top"),
+    (256, 24, 56, 1, 1, 2, "dup"), (5, 48, 600, 8, 2, 3, "top"),
+]
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("T,H,I,E,E_l,K,how", CASES)
+def test_exact(T, H, I, E, E_l, K, how, mx4):
+    case = integer_case(T, H, I, E, E_l, K, how, T * 31 + H)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for rank in range(min(E // E_l, 3)):
+        ws = torch.full((mc2.mc2_moe_tokens_workspace_size(T, K, H, I),), 255, dtype=torch.uint8,
+                        device="cuda")
+        out = own(*case, mx4, ep_rank=rank, num_experts=E, workspace=ws, dev_err=err)
+        ref, mag, bad = ot.layer(*(f64(t) if t.dtype != torch.int32 else t.numpy() for t in case),
+                                 ep_rank=rank, num_experts=E)
+        assert mag.max() < 2.0 ** 38 and np.abs(ref).max() < 2.0 ** 22  # sums stay exact
+        want = torch.from_numpy(ref).to(BF)
+        off = (out.cpu() != want).nonzero()
+        assert len(off) == 0, (rank, len(off), off[:4])
+    assert bool(err.item() & mc2.MC2_DEVERR_EXPERT_ID) == (how == "bad")
+
+
+def drawn(T, H, I, E, E_l, K, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((T, H), generator=g).to(BF)
+    w1 = (0.02 * torch.randn((E_l, H, 2 * I), generator=g)).to(BF)
+    w2 = (0.02 * torch.randn((E_l, I, H), generator=g)).to(BF)
+    logits = torch.randn((T, E), generator=g)
+    probs, sel = torch.softmax(logits, 1).topk(K, 1)
+    return x, sel.to(torch.int32), probs.contiguous(), w1, w2
+
+
+def close(out, ref):
+    """One rounding to bf16 (2^-8 of the value at most) on top of errors of the
+    32-bit sums and of the 16-bit h, some 2^-16 of the result's size: 2^-12 of
+    its root mean square covers them."""
+    ref = torch.as_tensor(ref)
+    err = (out.double().cpu() - ref).abs()
+    assert (err <= 2.0 ** -8 * ref.abs() + 2.0 ** -12 * ref.square().mean().sqrt()).all()
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("T,H,I,E,E_l,K", [(1, 512, 264, 16, 16, 4), (20, 264, 392, 8, 4, 3),
+                                           (70, 136, 128, 4, 4, 2)])
+def test_drawn(T, H, I, E, E_l, K, mx4):
+    case = list(drawn(T, H, I, E, E_l, K, 3))
+    out = own(*case, mx4, ep_rank=0, num_experts=E)
+    if mx4:  # the layer of the weights that the codes stand for
+        for i in (3, 4):
+            c, s = mc2.mc2_mx4_quantize(case[i].cuda(), trans=True)
+            case[i] = mc2.mc2_mx4_dequantize(c, s, case[i].shape[1], trans=True,
+                                             out_dtype=torch.float32).cpu()
+    ref, _, _ = ot.layer(*(f64(t) if t.dtype != torch.int32 else t.numpy() for t in case),
+                         ep_rank=0, num_experts=E)
+    close(out, ref)
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("T", [3, 40])
+def test_faults_stay_where_they_are(T, mx4):
+    """NaN and infinities in one token, in experts that no slot names, and in
+    the routing weights of slots that are not local reach no other output."""
+    H, I, E, E_l, K = 136, 72, 16, 8, 4
+    x, sel, probs, w1, w2 = integer_case(T, H, I, E, E_l, K, "top", 5)
+    sel = torch.where((sel % 8 == 3), sel + 1, sel)  # experts 3 and 11 are not named
+    args = dict(ep_rank=0, num_experts=E)
+    base = own(x, sel, probs, w1, w2, mx4, **args).cpu()
+    w1[3], w2[3] = float("nan"), float("inf")
+    probs = torch.where(sel >= E_l, float("nan"), probs)
+    sel[2] = 1
+    x[2, 5] = float("nan")
+    out = own(x, sel, probs, w1, w2, mx4, **args).cpu()
+    assert out[2].isnan().all()
+    keep = torch.arange(T) != 2
+    assert torch.equal(out[keep], base[keep])
+    sel[:] = E - 1  # no slot is local
+    assert (own(x, sel, probs, w1, w2, mx4, **args) == 0).all()
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("T", [1, 33])
+def test_captured_and_replayed(T, mx4):
+    """Replays with other tokens, routing and workspace contents give the eager
+    bits, with the program's own eager calls between them."""
+    H, I, E, K = 264, 136, 16, 4
+    cases = [integer_case(T, H, I, E, E, K, "top", s) for s in (1, 2)]
+    x, sel, probs, w1, w2 = (t.cuda() for t in cases[0])
+    kw = dict(ep_rank=0, num_experts=E)
+    if mx4:
+        (w1, s1), (w2, s2) = (mc2.mc2_mx4_quantize(w, trans=True) for w in (w1, w2))
+        kw.update(w1_scale=s1, w2_scale=s2)
+    out = torch.empty_like(x)
+    ws = torch.empty(mc2.mc2_moe_tokens_workspace_size(T, K, H, I), dtype=torch.uint8, device="cuda")
+
+    def call():
+        mc2.mc2_moe_tokens(x, sel, probs, w1, w2, out=out, workspace=ws, **kw)
+
+    def load(c):
+        for t, v in zip((x, sel, probs), c):
+            t.copy_(v)
+
+    eager = []
+    for c in cases:
+        load(c)
+        call()
+        eager.append(out.clone())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for i in (0, 1, 1, 0):
+        load(cases[i])
+        ws.fill_(255)
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[i])
+        call()
+        assert torch.equal(out, eager[i])
+
+
+def test_two_streams_with_a_workspace_each():
+    T, H, I, E, K = 24, 264, 136, 16, 4
+    cases = [tuple(t.cuda() for t in integer_case(T, H, I, E, E, K, "top", s)) for s in (3, 4)]
+    want = [mc2.mc2_moe_tokens(*c, ep_rank=0, num_experts=E) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[], []]
+    for _ in range(20):
+        for i, (s, c) in enumerate(zip(streams, cases)):
+            with torch.cuda.stream(s):
+                outs[i].append(mc2.mc2_moe_tokens(*c, ep_rank=0, num_experts=E))
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(v, w) for v in o)
+
+
+def test_agrees_with_the_path_for_many_tokens():
+    """One set of 4-bit expert weights, both ways to use them: this layer on the
+    codes, and the grouped path (permute, fc1, fc2, unpermute) on the 16-bit
+    weights that they stand for. The grouped path rounds h and y to bf16."""
+    T, H, I, E, K = 48, 512, 264, 16, 4
+    x, sel, probs, w1, w2 = (t.cuda() for t in drawn(T, H, I, E, E, K, 9))
+    (c1, s1), (c2, s2) = (mc2.mc2_mx4_quantize(w, trans=True) for w in (w1, w2))
+    out = mc2.mc2_moe_tokens(x, sel, probs, c1, c2, w1_scale=s1, w2_scale=s2, ep_rank=0,
+                             num_experts=E)
+    w1 = mc2.mc2_mx4_dequantize(c1, s1, H, trans=True)
+    w2 = mc2.mc2_mx4_dequantize(c2, s2, I, trans=True)
+    counts = mc2.mc2_moe_histc(sel, E)
+    perm, _, uidx, _ = mc2.mc2_moe_permute(x, sel, E)
+    kw = dict(ep_rank=0, num_experts=E)
+    h = mc2.mc2_gmm_dispatch(perm, counts, counts, w1, **kw)
+    buf = torch.zeros((T * K, H), dtype=BF, device="cuda")
+    mc2.mc2_gmm_combine(h, counts, counts, w2, buf, **kw)
+    many = mc2.mc2_moe_unpermute(buf, uidx, probs)
+    # h and y are off by 2^-8 each at most, over sums of hundreds of terms and
+    # of K slots, and both outputs by one rounding
+    rms = out.double().square().mean().sqrt()
+    err = (out.double() - many.double()).abs()
+    assert (err <= 2.0 ** -7 * out.double().abs() + 2.0 ** -6 * rms).all()
+    assert err.square().mean().sqrt() <= 2.0 ** -8 * 1.5 * rms
