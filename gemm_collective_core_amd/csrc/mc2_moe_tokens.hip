@@ -13,10 +13,11 @@
 //     results y of a slot stay fp32 in the workspace; the workgroup that is the
 //     last of its strip adds them up per token, in slot order, with the weights.
 //
-// A workgroup finds its expert by itself: the a-th expert, in order of id, that a
-// slot names, and that expert's slots (no sorting launch, no count on the
-// host). Rows of the 16-row operand that no slot fills repeat the last one and
-// are dropped: rows of a product do not mix, so neither do their NaN.
+// A workgroup of fc1 finds its expert by itself, the a-th that a slot names, and
+// that expert's slots (no sorting launch, no count on the host); one workgroup
+// more writes the same as a plan for fc2. Rows of the 16-row operand that no
+// slot fills repeat the last one and are dropped: rows of a product do not mix,
+// so neither do their NaN.
 #include "mc2_mx4.hpp"
 #include "mc2_tiles.hpp"
 
@@ -25,6 +26,7 @@ namespace mc2 {
 constexpr int kTokMaxSlots = 4096;   // T * K
 constexpr int kTokMaxExperts = 1024;
 constexpr int kCpolAgent = 0x10;     // sc1: coherent over the XCDs' L2s
+constexpr int kTokMany = 2;          // 16-row operands at a time where an expert has more slots
 
 // Strips of fc2 at most: 16 columns each.
 __host__ __device__ constexpr int64_t tok_strips(int64_t H) { return (H + 15) / 16; }
@@ -39,6 +41,8 @@ struct TokArgs {
   const char* w2s;
   uint16_t* out;
   uint32_t* arrived;  // per strip of fc2
+  i32x4_t* plan;      // expert, slots, place of the first in list, experts named
+  uint16_t* list;     // local slots, expert after expert
   uint16_t* h_hi;
   uint16_t* h_lo;
   float* y;
@@ -47,36 +51,57 @@ struct TokArgs {
   int T, K, TK, E, e0, El;
 };
 
-// Which expert (of this rank's) a workgroup works for, its slots, and how many
-// experts are named at all.
+// Which expert (of this rank's) a workgroup works for, and how many slots of it.
 struct Expert {
-  int e, count, named;
+  int e, count;
 };
 
-template <int NT>
 struct PickMem {
   uint32_t words[kTokMaxExperts / 32];
   int count;
   uint16_t list[kTokMaxSlots];
 };
 
-// Expert number `a` of those named, in order of id (e = -1 past the last), and
-// its slots in mem.list, in any order: rows of a product do not mix.
+__device__ __forceinline__ int local_id(const TokArgs& p, int s) {
+  const int e = p.sel[s] - p.e0;
+  return s < p.TK && e >= 0 && e < p.El ? e : -1;
+}
+
+// The a-th expert named (e = -1 past the last) and its slots in mem.list, in any
+// order: rows of a product do not mix.
+//   Up to 64 slots: a lane each, no barrier. Experts count in the order of their
+// first slot; every wave finds the same and writes the same list.
+//   More: experts count in the order of their ids, through a bit set in LDS.
 template <int NT>
-__device__ __forceinline__ Expert pick_expert(const TokArgs& p, int a, PickMem<NT>& mem) {
-  constexpr int PER = kTokMaxSlots / NT;
+__device__ __forceinline__ Expert pick_expert(const TokArgs& p, int a, PickMem& mem) {
   const int lane = threadIdx.x & 63;
+  Expert r{-1, 0};
+  if (p.TK <= 64) {
+    const int id = local_id(p, lane < p.TK ? lane : p.TK - 1);
+    const uint64_t valid = __ballot(id >= 0 && lane < p.TK);
+    uint64_t left = valid;
+    for (;; --a) {
+      if (left == 0) return r;
+      const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+      const uint64_t same = __ballot(id == e) & valid;
+      left &= ~same;
+      if (a == 0) {
+        if ((same >> lane) & 1)
+          mem.list[__popcll(same & ((uint64_t{1} << lane) - 1))] = static_cast<uint16_t>(lane);
+        r.e = e;
+        r.count = __popcll(same);
+        return r;
+      }
+    }
+  }
+  constexpr int PER = kTokMaxSlots / NT;
   if (threadIdx.x < kTokMaxExperts / 32) mem.words[threadIdx.x] = 0;
   if (threadIdx.x == 0) mem.count = 0;
   int id[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int s = threadIdx.x + i * NT;
-    id[i] = -1;
-    if (i * NT < p.TK && s < p.TK) {
-      const int e = p.sel[s] - p.e0;
-      id[i] = e >= 0 && e < p.El ? e : -1;
-    }
+    id[i] = i * NT < p.TK && s < p.TK ? local_id(p, s) : -1;
   }
   __syncthreads();
 #pragma unroll
@@ -91,11 +116,7 @@ __device__ __forceinline__ Expert pick_expert(const TokArgs& p, int a, PickMem<N
     const int o = __shfl_up(sum, d);
     if (lane >= d && lane < 32) sum += o;
   }
-  Expert r;
-  r.named = __builtin_amdgcn_readlane(sum, 31);
-  r.e = -1;
-  r.count = 0;
-  if (a >= r.named) return r;  // uniform over the workgroup
+  if (a >= __builtin_amdgcn_readlane(sum, 31)) return r;  // uniform over the workgroup
   const int before = sum - __popc(w);
   const uint64_t mine = __ballot(lane < 32 && before <= a && a < sum);
   const int wl = __builtin_ctzll(mine);
@@ -108,6 +129,56 @@ __device__ __forceinline__ Expert pick_expert(const TokArgs& p, int a, PickMem<N
   __syncthreads();
   r.count = __builtin_amdgcn_readfirstlane(mem.count);
   return r;
+}
+
+// The plan of fc2, by one workgroup: every expert named, in order of id, with its
+// slots; the arrival counters cleared; ids out of range reported.
+template <int NT>
+__device__ __forceinline__ void write_plan(const TokArgs& p, int slots) {
+  __shared__ int cnt[kTokMaxExperts];  // slots of an expert, then the next place of its list
+  const int lane = threadIdx.x & 63;
+  for (int64_t i = threadIdx.x; i < tok_strips(p.H); i += NT) p.arrived[i] = 0;
+  for (int i = threadIdx.x; i < kTokMaxExperts; i += NT) cnt[i] = 0;
+  __syncthreads();
+  for (int s = threadIdx.x; s < p.TK; s += NT) {
+    const int e = local_id(p, s);
+    if (e >= 0) atomicAdd(&cnt[e], 1);
+    if (p.sel[s] < 0 || p.sel[s] >= p.E) atomic_or_err(p.dev_err, MC2_DEVERR_EXPERT_ID);
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    constexpr int PER = kTokMaxExperts / 64;  // neighbours a lane
+    int named = 0, rows = 0;
+    for (int i = 0; i < PER; ++i) {
+      const int c = cnt[lane * PER + i];
+      named += c > 0;
+      rows += c;
+    }
+    int n = named, r = rows;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int on = __shfl_up(n, d), orr = __shfl_up(r, d);
+      if (lane >= d) {
+        n += on;
+        r += orr;
+      }
+    }
+    const int total = __builtin_amdgcn_readlane(n, 63);
+    n -= named;
+    r -= rows;
+    for (int i = 0; i < PER; ++i) {
+      const int c = cnt[lane * PER + i];
+      if (c > 0) p.plan[n++] = i32x4_t{lane * PER + i, c, r, total};
+      cnt[lane * PER + i] = r;
+      r += c;
+    }
+    for (int i = total + lane; i < slots; i += 64) p.plan[i] = i32x4_t{-1, 0, 0, total};
+  }
+  __syncthreads();
+  for (int s = threadIdx.x; s < p.TK; s += NT) {
+    const int e = local_id(p, s);
+    if (e >= 0) p.list[atomicAdd(&cnt[e], 1)] = static_cast<uint16_t>(s);
+  }
 }
 
 // ------------------------------------------------------------------- weights
@@ -329,19 +400,18 @@ __device__ __forceinline__ void fc1_rows(const TokArgs& p, const uint16_t* list,
   __syncthreads();
 }
 
-// MANY: more than 16 tokens, so that an expert may have more than 16 slots
-// of different tokens; they are then taken 64 at a time.
+// MANY: more than 16 tokens, so that an expert may have more than 16 slots of
+// different tokens; they are then taken 32 at a time.
 template <class W, bool MANY>
 __global__ __launch_bounds__(W::NW * 64) void tokens_fc1_kernel(TokArgs p) {
   constexpr int NT = W::NW * 64;
-  __shared__ PickMem<NT> mem;
+  __shared__ PickMem mem;
   __shared__ f32x4_t red[W::NW][2 * W::NF][64];
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    for (int64_t i = threadIdx.x; i < tok_strips(p.H); i += NT) p.arrived[i] = 0;
-    for (int s = threadIdx.x; s < p.TK; s += NT)
-      if (p.sel[s] < 0 || p.sel[s] >= p.E) atomic_or_err(p.dev_err, MC2_DEVERR_EXPERT_ID);
+  if (blockIdx.y == 0) {  // a row of workgroups ahead of the experts': the plan
+    if (blockIdx.x == 0) write_plan<NT>(p, gridDim.y - 1);
+    return;
   }
-  const Expert ex = pick_expert<NT>(p, blockIdx.y, mem);
+  const Expert ex = pick_expert<NT>(p, blockIdx.y - 1, mem);
   if (ex.e < 0) return;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * (16 * W::NF);
   const auto sg = W::strip(p.w1, p.w1s, ex.e, p.H, 2 * p.I, 0, c0, p.I);
@@ -349,8 +419,9 @@ __global__ __launch_bounds__(W::NW * 64) void tokens_fc1_kernel(TokArgs p) {
   for (int b = 0; b < ex.count;) {
     const int left = ex.count - b;
     if (MANY && left > 16) {
-      fc1_rows<W, 4>(p, mem.list + b, left < 64 ? left : 64, sg, su, c0, red);
-      b += 64;
+      fc1_rows<W, kTokMany>(p, mem.list + b, left < 16 * kTokMany ? left : 16 * kTokMany, sg, su,
+                            c0, red);
+      b += 16 * kTokMany;
     } else {
       fc1_rows<W, 1>(p, mem.list + b, left < 16 ? left : 16, sg, su, c0, red);
       b += 16;
@@ -444,14 +515,25 @@ __device__ __forceinline__ void sum_slots(const TokArgs& p, int64_t c0, int cw) 
     const int64_t c = c0 + 4 * (q - t * q4);
     if (c >= p.H) continue;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < p.K; ++k) {
-      const int s = t * p.K + k, e = p.sel[s] - p.e0;
-      if (e < 0 || e >= p.El) continue;
-      const float w = p.probs[s];
-      const u32x4_t y = __builtin_amdgcn_raw_buffer_load_b128(
-          ry, static_cast<int>((static_cast<int64_t>(s) * p.H + c) * 4), 0, kCpolAgent);
+    for (int k0 = 0; k0 < p.K; k0 += 8) {  // eight slots' loads in flight
+      u32x4_t y[8];
+      float w[8];
+      bool in[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(w, __uint_as_float(y[j]), v[j]);
+      for (int j = 0; j < 8; ++j) {
+        const int s = t * p.K + (k0 + j < p.K ? k0 + j : p.K - 1);
+        in[j] = k0 + j < p.K && local_id(p, s) >= 0;
+        w[j] = p.probs[s];
+        y[j] = __builtin_amdgcn_raw_buffer_load_b128(
+            ry, in[j] ? static_cast<uint32_t>((static_cast<int64_t>(s) * p.H + c) * 4) : kOffNone, 0,
+            kCpolAgent);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (in[j]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(w[j], __uint_as_float(y[j][i]), v[i]);
+        }
     }
     *reinterpret_cast<u32x2_t*>(p.out + static_cast<int64_t>(t) * p.H + c) = pack4<Out::BF16>(v);
   }
@@ -460,36 +542,36 @@ __device__ __forceinline__ void sum_slots(const TokArgs& p, int64_t c0, int cw) 
 template <class W, bool MANY>
 __global__ __launch_bounds__(W::NW * 64) void tokens_fc2_kernel(TokArgs p) {
   constexpr int NT = W::NW * 64, CW = 16 * W::NF;
-  __shared__ PickMem<NT> mem;
   __shared__ f32x4_t red[W::NW][W::NF][64];
   __shared__ int last;
-  const Expert ex = pick_expert<NT>(p, blockIdx.y, mem);
+  const i32x4_t plan = p.plan[blockIdx.y];
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * CW;
-  if (ex.e < 0) {
+  const int count = plan[1], named = plan[3];
+  if (plan[0] < 0) {
     // no slot is local: the output is zeros
-    if (ex.named == 0 && blockIdx.y == 0) sum_slots<NT>(p, c0, CW);
+    if (named == 0 && blockIdx.y == 0) sum_slots<NT>(p, c0, CW);
     return;
   }
-  const auto sw = W::strip(p.w2, p.w2s, ex.e, p.I, p.H, 0, c0, p.H);
-  for (int b = 0; b < ex.count;) {
-    const int left = ex.count - b;
+  const auto sw = W::strip(p.w2, p.w2s, plan[0], p.I, p.H, 0, c0, p.H);
+  const uint16_t* list = p.list + plan[2];
+  for (int b = 0; b < count;) {
+    const int left = count - b;
     if (MANY && left > 16) {
-      fc2_rows<W, 4>(p, mem.list + b, left < 64 ? left : 64, sw, c0, red);
-      b += 64;
+      fc2_rows<W, kTokMany>(p, list + b, left < 16 * kTokMany ? left : 16 * kTokMany, sw, c0, red);
+      b += 16 * kTokMany;
     } else {
-      fc2_rows<W, 1>(p, mem.list + b, left < 16 ? left : 16, sw, c0, red);
+      fc2_rows<W, 1>(p, list + b, left < 16 ? left : 16, sw, c0, red);
       b += 16;
     }
   }
+  // y was written through to memory and is read from there: once the stores
+  // are done (the wait), no cache needs a write-back or an invalidation, which
+  // would cost the other workgroups their weights
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    const uint32_t before = __hip_atomic_fetch_add(&p.arrived[blockIdx.x], 1u, __ATOMIC_RELAXED,
-                                                   __HIP_MEMORY_SCOPE_AGENT);
-    last = before + 1 == static_cast<uint32_t>(ex.named);
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  }
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(&p.arrived[blockIdx.x], 1u, __ATOMIC_RELAXED,
+                                  __HIP_MEMORY_SCOPE_AGENT) + 1 == static_cast<uint32_t>(named);
   __syncthreads();
   if (last) sum_slots<NT>(p, c0, CW);
 }
@@ -497,7 +579,7 @@ __global__ __launch_bounds__(W::NW * 64) void tokens_fc2_kernel(TokArgs p) {
 // ------------------------------------------------------------------ host side
 
 struct TokWorkspace {
-  size_t arrived, h, y, bytes;
+  size_t arrived, plan, list, h, y, bytes;
 };
 
 static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -508,7 +590,9 @@ static bool tok_workspace(int64_t T, int K, int64_t H, int64_t I, TokWorkspace& 
   const int64_t TK = T * K;
   if (TK * H >= int64_t{1} << 28 || TK * I >= int64_t{1} << 28) return false;
   w.arrived = 0;
-  w.h = up256(static_cast<size_t>(tok_strips(H)) * 4);
+  w.plan = up256(static_cast<size_t>(tok_strips(H)) * 4);
+  w.list = w.plan + up256(static_cast<size_t>(TK < kTokMaxExperts ? TK : kTokMaxExperts) * 16);
+  w.h = w.list + up256(static_cast<size_t>(TK) * 2);
   w.y = w.h + up256(static_cast<size_t>(TK * I) * 2) * 2;
   w.bytes = w.y + up256(static_cast<size_t>(TK * H) * 4);
   return true;
@@ -516,7 +600,7 @@ static bool tok_workspace(int64_t T, int K, int64_t H, int64_t I, TokWorkspace& 
 
 template <class W, bool MANY>
 static void launch_fc1(const TokArgs& a, int slots, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.I + 16 * W::NF - 1) / (16 * W::NF)), slots);
+  const dim3 grid(static_cast<unsigned>((a.I + 16 * W::NF - 1) / (16 * W::NF)), slots + 1);
   hipLaunchKernelGGL((tokens_fc1_kernel<W, MANY>), grid, dim3(W::NW * 64), 0, s, a);
 }
 template <class W, bool MANY>
@@ -534,7 +618,7 @@ static void launch_tokens(const TokArgs& a, bool mx4, hipStream_t s) {
   if (mx4) {
     if (wide1) launch_fc1<WMx4<2>, MANY>(a, slots, s);
     else launch_fc1<WMx4<1>, MANY>(a, slots, s);
-    if (wide2) launch_fc2<WMx4<2>, MANY>(a, slots, s);
+    if (wide2) launch_fc2<WMx4<4>, MANY>(a, slots, s);
     else launch_fc2<WMx4<1>, MANY>(a, slots, s);
   } else {
     if (wide1) launch_fc1<WBf16<4>, MANY>(a, slots, s);
@@ -584,6 +668,8 @@ extern "C" int mc2_moe_tokens(const void* x, const int32_t* sel, const float* pr
   a.w2s = static_cast<const char*>(w2_scale);
   a.out = static_cast<uint16_t*>(out);
   a.arrived = reinterpret_cast<uint32_t*>(ws + w.arrived);
+  a.plan = reinterpret_cast<i32x4_t*>(ws + w.plan);
+  a.list = reinterpret_cast<uint16_t*>(ws + w.list);
   a.h_hi = reinterpret_cast<uint16_t*>(ws + w.h);
   a.h_lo = reinterpret_cast<uint16_t*>(ws + w.h + (w.y - w.h) / 2);
   a.y = reinterpret_cast<float*>(ws + w.y);
