@@ -10,14 +10,16 @@
 //     of H; the waves' sums meet in LDS, SwiGLU follows, and h leaves as the sum
 //     of two bf16 numbers.
 //   tokens_fc2_kernel: the same with h and w2 for a strip of output columns. The
-//     results y of a slot stay fp32 in the workspace; the workgroup that is the
-//     last of its strip adds them up per token, in slot order, with the weights.
+//     results y of a slot stay fp32 in the workspace; the workgroup that brings
+//     the last one of a token adds the token's strip up, in slot order, with the
+//     routing weights.
 //
 // A workgroup of fc1 finds its expert by itself, the a-th that a slot names, and
-// that expert's slots (no sorting launch, no count on the host); one workgroup
-// more writes the same as a plan for fc2. Rows of the 16-row operand that no
-// slot fills repeat the last one and are dropped: rows of a product do not mix,
-// so neither do their NaN.
+// that expert's slots (no sorting launch, no count on the host); a row of
+// workgroups more writes what fc2 needs: the same as a plan, and each token's
+// count of local slots. Rows of the 16-row operand that no slot fills are zeros,
+// which load nothing, and are dropped: rows of a product do not mix, so neither
+// do their NaN.
 #include "mc2_mx4.hpp"
 #include "mc2_tiles.hpp"
 
@@ -26,6 +28,7 @@ namespace mc2 {
 constexpr int kTokMaxSlots = 4096;   // T * K
 constexpr int kTokMaxExperts = 1024;
 constexpr int kCpolAgent = 0x10;     // sc1: coherent over the XCDs' L2s
+constexpr int kTokMaxPer = 64;       // strips a workgroup
 constexpr int kTokMany = 2;          // 16-row operands at a time where an expert has more slots
 
 // Strips of fc2 at most: 16 columns each.
@@ -40,7 +43,7 @@ struct TokArgs {
   const char* w2;
   const char* w2s;
   uint16_t* out;
-  uint32_t* arrived;  // per strip of fc2
+  int32_t* left;      // (strip of fc2, token): local slots whose y is still to come
   i32x4_t* plan;      // expert, slots, place of the first in list, experts named
   uint16_t* list;     // local slots, expert after expert
   uint16_t* h_hi;
@@ -49,6 +52,7 @@ struct TokArgs {
   int32_t* dev_err;
   int64_t H, I;
   int T, K, TK, E, e0, El;
+  int strips1, strips2, per1, per2;  // strips of a matrix, and of a workgroup
 };
 
 // Which expert (of this rank's) a workgroup works for, and how many slots of it.
@@ -57,7 +61,6 @@ struct Expert {
 };
 
 struct PickMem {
-  uint32_t words[kTokMaxExperts / 32];
   int count;
   uint16_t list[kTokMaxSlots];
 };
@@ -67,11 +70,12 @@ __device__ __forceinline__ int local_id(const TokArgs& p, int s) {
   return s < p.TK && e >= 0 && e < p.El ? e : -1;
 }
 
-// The a-th expert named (e = -1 past the last) and its slots in mem.list, in any
-// order: rows of a product do not mix.
-//   Up to 64 slots: a lane each, no barrier. Experts count in the order of their
-// first slot; every wave finds the same and writes the same list.
-//   More: experts count in the order of their ids, through a bit set in LDS.
+// The expert of row `a` of workgroups (e = -1: none) and its slots in mem.list,
+// in any order: rows of a product do not mix.
+//   Up to 64 slots: the a-th expert that they name, in the order of their first
+// slots; a lane each and no barrier, every wave finds the same and writes the
+// same list.
+//   More: expert a, of which the row may find no slot.
 template <int NT>
 __device__ __forceinline__ Expert pick_expert(const TokArgs& p, int a, PickMem& mem) {
   const int lane = threadIdx.x & 63;
@@ -94,50 +98,22 @@ __device__ __forceinline__ Expert pick_expert(const TokArgs& p, int a, PickMem& 
       }
     }
   }
-  constexpr int PER = kTokMaxSlots / NT;
-  if (threadIdx.x < kTokMaxExperts / 32) mem.words[threadIdx.x] = 0;
   if (threadIdx.x == 0) mem.count = 0;
-  int id[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int s = threadIdx.x + i * NT;
-    id[i] = i * NT < p.TK && s < p.TK ? local_id(p, s) : -1;
-  }
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (id[i] >= 0) atomicOr(&mem.words[id[i] >> 5], 1u << (id[i] & 31));
-  __syncthreads();
-  // every wave: lanes hold the words, their running count of bits
-  const uint32_t w = lane < kTokMaxExperts / 32 ? mem.words[lane] : 0u;
-  int sum = __popc(w);
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up(sum, d);
-    if (lane >= d && lane < 32) sum += o;
-  }
-  if (a >= __builtin_amdgcn_readlane(sum, 31)) return r;  // uniform over the workgroup
-  const int before = sum - __popc(w);
-  const uint64_t mine = __ballot(lane < 32 && before <= a && a < sum);
-  const int wl = __builtin_ctzll(mine);
-  uint32_t bits = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(w), wl));
-  for (int skip = a - __builtin_amdgcn_readlane(before, wl); skip > 0; --skip) bits &= bits - 1;
-  r.e = __builtin_amdgcn_readfirstlane(wl * 32 + __builtin_ctz(bits));
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (id[i] == r.e) mem.list[atomicAdd(&mem.count, 1)] = static_cast<uint16_t>(threadIdx.x + i * NT);
+  for (int s = threadIdx.x; s < p.TK; s += NT)
+    if (p.sel[s] - p.e0 == a) mem.list[atomicAdd(&mem.count, 1)] = static_cast<uint16_t>(s);
   __syncthreads();
   r.count = __builtin_amdgcn_readfirstlane(mem.count);
+  if (r.count > 0) r.e = a;
   return r;
 }
 
 // The plan of fc2, by one workgroup: every expert named, in order of id, with its
-// slots; the arrival counters cleared; ids out of range reported.
+// slots; ids out of range reported.
 template <int NT>
 __device__ __forceinline__ void write_plan(const TokArgs& p, int slots) {
   __shared__ int cnt[kTokMaxExperts];  // slots of an expert, then the next place of its list
   const int lane = threadIdx.x & 63;
-  for (int64_t i = threadIdx.x; i < tok_strips(p.H); i += NT) p.arrived[i] = 0;
   for (int i = threadIdx.x; i < kTokMaxExperts; i += NT) cnt[i] = 0;
   __syncthreads();
   for (int s = threadIdx.x; s < p.TK; s += NT) {
@@ -181,13 +157,29 @@ __device__ __forceinline__ void write_plan(const TokArgs& p, int slots) {
   }
 }
 
+// Token t's counters of every strip of fc2, or its row of zeros where no slot of
+// it is local.
+template <int NT>
+__device__ __forceinline__ void count_slots(const TokArgs& p, int t) {
+  const int lane = threadIdx.x & 63;  // K is 64 at most
+  const int n = __popcll(__ballot(lane < p.K && local_id(p, t * p.K + (lane < p.K ? lane : 0)) >= 0));
+  for (int s = threadIdx.x; s < p.strips2; s += NT) p.left[s * p.T + t] = n;
+  if (n == 0)
+    for (int64_t c = threadIdx.x * 8; c < p.H; c += NT * 8)
+      *reinterpret_cast<u32x4_t*>(p.out + t * p.H + c) = zero_v4();
+}
+
 // ------------------------------------------------------------------- weights
 //
-// A step of K for a strip of 16 * NF columns of one matrix: load() brings this
-// lane's part into registers, frag<T>(f) is the operand of fragment f (16
-// columns) for sub-step T of KT, 32 K values each. k0(s, T, g): first of the
-// eight K values that lane group g holds of it. Column c of the strip is lane
-// lane_of(c) & 15 of fragment frag_of(c).
+// The weights of a strip of 16 * NF columns of one matrix, KS of K a step, taken
+// in groups of U neighbouring steps a wave: Group holds this lane's part of one.
+// load(st, step, u) brings step u of a group into registers and scales(st, step)
+// what its U steps share, which take() puts in force; frag<T>(u, f) is the
+// operand of fragment f (16 columns) for sub-step T of KT, 32 K values each.
+// k0(s, T, g): first of the eight K values that lane group g holds of it.
+// Column c of the strip is lane lane_of(c) & 15 of fragment frag_of(c).
+// (Addresses are 32-bit offsets from scalar bases: 64-bit ones would take two
+// registers for each load in flight.)
 
 // bf16 weights (rows of K, columns contiguous): a lane loads LC neighbouring
 // columns of eight K rows; the eight values of a column then lie in one lane
@@ -196,8 +188,7 @@ __device__ __forceinline__ void write_plan(const TokArgs& p, int slots) {
 template <int LC_>
 struct WBf16 {
   static constexpr int NF = LC_, LC = LC_, KS = 32, KT = 1, NW = 8;
-  static constexpr int U = LC_ == 2 ? 4 : 2;  // steps in flight
-  uint32_t r[8][LC_ / 2];
+  static constexpr int U1 = LC_ == 2 ? 4 : 2, U2 = 4;  // steps a group, fc1 and fc2
 
   struct Strip {
     const char* base;  // column 0 of the strip in K row 0
@@ -214,33 +205,37 @@ struct WBf16 {
             static_cast<uint32_t>((8 * (lane >> 4) * cols + (mine < most ? mine : most)) * 2),
             static_cast<uint32_t>(cols * 2), K};
   }
-  // (32-bit offsets from a scalar base: 64-bit addresses would take two
-  // registers for each load in flight)
-  __device__ __forceinline__ void load(const Strip& st, int64_t s) {
-    const int64_t row = s * 32 + 8 * ((threadIdx.x & 63) >> 4);
-    // k is a multiple of 8: all eight rows or none
-    const uint32_t off = row < st.k ? st.off : kOffNone;
-    const __amdgpu_buffer_rsrc_t q = make_rsrc(st.base + s * 32 * st.ld);
+  template <int U>
+  struct Group {
+    uint32_t r[U][8][LC_ / 2];
+    __device__ __forceinline__ void load(const Strip& st, int64_t s, int u) {
+      const int64_t row = s * 32 + 8 * ((threadIdx.x & 63) >> 4);
+      // k is a multiple of 8: all eight rows or none
+      const uint32_t off = row < st.k ? st.off : kOffNone;
+      const __amdgpu_buffer_rsrc_t q = make_rsrc(st.base + s * 32 * st.ld);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (LC == 4) {
-        const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(q, off, i * st.ld, 0);
-        r[i][0] = v[0];
-        r[i][1] = v[1];
-      } else {
-        r[i][0] = __builtin_amdgcn_raw_buffer_load_b32(q, off, i * st.ld, 0);
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (LC == 4) {
+          const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(q, off, i * st.ld, 0);
+          r[u][i][0] = v[0];
+          r[u][i][1] = v[1];
+        } else {
+          r[u][i][0] = __builtin_amdgcn_raw_buffer_load_b32(q, off, i * st.ld, 0);
+        }
       }
     }
-  }
-  template <int T>
-  __device__ __forceinline__ bf16x8_t frag(int f) const {
-    u32x4_t v;
+    __device__ __forceinline__ void scales(const Strip&, int64_t) {}
+    __device__ __forceinline__ void take() {}
+    template <int T>
+    __device__ __forceinline__ bf16x8_t frag(int u, int f) const {
+      u32x4_t v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = __builtin_amdgcn_perm(r[2 * i + 1][f >> 1], r[2 * i][f >> 1],
-                                   (f & 1) ? 0x07060302u : 0x05040100u);
-    return bit_cast<bf16x8_t>(v);
-  }
+      for (int i = 0; i < 4; ++i)
+        v[i] = __builtin_amdgcn_perm(r[u][2 * i + 1][f >> 1], r[u][2 * i][f >> 1],
+                                     (f & 1) ? 0x07060302u : 0x05040100u);
+      return bit_cast<bf16x8_t>(v);
+    }
+  };
   static __device__ __forceinline__ int64_t k0(int64_t s, int, int g) { return s * 32 + 8 * g; }
   static __device__ __forceinline__ int frag_of(int c) { return c % LC; }
   static __device__ __forceinline__ int lane_of(int c) { return c / LC; }
@@ -248,18 +243,18 @@ struct WBf16 {
 
 // MX4 weights (a row per column, K contiguous): a lane holds a block of 32 K
 // values of each of its NF columns, 16 n + the fragment's first, and turns eight
-// of them at a time into exact bf16 numbers.
+// of them at a time into exact bf16 numbers. The four scale bytes of a step's
+// blocks are one dword of the row, and those of a group's steps one load (a
+// byte load for each step and fragment took 30 of 171 us at 64 tokens).
 template <int NF_>
 struct WMx4 {
   static constexpr int NF = NF_, KS = 128, KT = 4, NW = 4;
-  static constexpr int U = 2;
-  u32x4_t c[NF_];
-  float s[NF_];
+  static constexpr int U1 = 4, U2 = 2;
 
   struct Strip {
     const char* base;
     const char* sbase;
-    uint32_t off[NF_], soff[NF_];  // this lane's column and block g
+    uint32_t off[NF_], soff[NF_];  // this lane's column: block g, scales
     int64_t nb;
   };
   static __device__ __forceinline__ Strip strip(const char* w, const char* ws, int64_t e, int64_t K,
@@ -276,24 +271,53 @@ struct WMx4 {
       const int64_t mine = 16 * f + (lane & 15), most = limit - 1 - c0;
       const int64_t c = mine < most ? mine : most;
       st.off[f] = static_cast<uint32_t>((c * st.nb + (lane >> 4)) * 16);
-      st.soff[f] = static_cast<uint32_t>(c * pitch + (lane >> 4));
+      st.soff[f] = static_cast<uint32_t>(c * pitch);
     }
     return st;
   }
-  __device__ __forceinline__ void load(const Strip& st, int64_t step) {
-    const bool in = step * 4 + ((threadIdx.x & 63) >> 4) < st.nb;
-    const __amdgpu_buffer_rsrc_t q = make_rsrc(st.base + step * 64);
-    const __amdgpu_buffer_rsrc_t qs = make_rsrc(st.sbase + step * 4);
+  template <int U>
+  struct Group {
+    static_assert(U == 1 || U == 2 || U == 4, "scales of a group in one load");
+    u32x4_t c[U][NF_];
+    uint32_t sc[NF_][U], nx[NF_][U];
+    __device__ __forceinline__ void load(const Strip& st, int64_t s, int u) {
+      const bool in = s * 4 + ((threadIdx.x & 63) >> 4) < st.nb;
+      const __amdgpu_buffer_rsrc_t q = make_rsrc(st.base + s * 64);
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      c[f] = __builtin_amdgcn_raw_buffer_load_b128(q, in ? st.off[f] : kOffNone, 0, 0);
-      s[f] = mx4_scale(__builtin_amdgcn_raw_buffer_load_b8(qs, in ? st.soff[f] : kOffNone, 0, 0));
+      for (int f = 0; f < NF; ++f)
+        c[u][f] = __builtin_amdgcn_raw_buffer_load_b128(q, in ? st.off[f] : kOffNone, 0, 0);
     }
-  }
-  template <int T>
-  __device__ __forceinline__ bf16x8_t frag(int f) const {
-    return bit_cast<bf16x8_t>(mx4_bf16x8(c[f][T], s[f]));
-  }
+    // s: the group's first step, a multiple of U
+    __device__ __forceinline__ void scales(const Strip& st, int64_t s) {
+      const __amdgpu_buffer_rsrc_t q = make_rsrc(st.sbase + s * 4);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const uint32_t off = s * 4 < st.nb ? st.soff[f] : kOffNone;
+        if constexpr (U == 4) {
+          const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(q, off, 0, 0);
+#pragma unroll
+          for (int u = 0; u < U; ++u) nx[f][u] = v[u];
+        } else if constexpr (U == 2) {
+          const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(q, off, 0, 0);
+          nx[f][0] = v[0];
+          nx[f][U - 1] = v[1];
+        } else {
+          nx[f][0] = __builtin_amdgcn_raw_buffer_load_b32(q, off, 0, 0);
+        }
+      }
+    }
+    __device__ __forceinline__ void take() {
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int u = 0; u < U; ++u) sc[f][u] = nx[f][u];
+    }
+    template <int T>
+    __device__ __forceinline__ bf16x8_t frag(int u, int f) const {
+      const uint32_t byte = (sc[f][u] >> (((threadIdx.x & 63) >> 4) * 8)) & 255u;
+      return bit_cast<bf16x8_t>(mx4_bf16x8(c[u][f][T], mx4_scale(byte)));
+    }
+  };
   static __device__ __forceinline__ int64_t k0(int64_t s, int t, int g) {
     return s * 128 + 32 * g + 8 * t;
   }
@@ -303,6 +327,11 @@ struct WMx4 {
 
 __device__ __forceinline__ f32x4_t mfma_bf16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Workgroup barrier for LDS alone: loads from memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // The waves' sums of NV values a lane (one 16-row tile), through LDS: element
@@ -317,113 +346,156 @@ __device__ __forceinline__ float tile_sum(const f32x4_t (&red)[NW][NV][64], int 
 
 // ----------------------------------------------------------------------- fc1
 
-// h of up to 16 * MT slots, list[0 .. count), of the strip's columns.
+// Both kernels walk the strips [s0, s1) of one expert with the loads a group of
+// U K steps ahead: a step's registers are loaded again for the next group, of
+// this strip or the next, as soon as its products are done, so that memory is
+// read on while the waves' sums meet in LDS. Where one group covers K, the rows'
+// operands are loaded once for all strips.
+
+// h of up to 16 * MT slots, list[0 .. count).
 template <class W, int MT>
-__device__ __forceinline__ void fc1_rows(const TokArgs& p, const uint16_t* list, int count,
-                                         const typename W::Strip& sg, const typename W::Strip& su,
-                                         int64_t c0, f32x4_t (&red)[W::NW][2 * W::NF][64]) {
-  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U : 1;
+__device__ __forceinline__ void fc1_rows(const TokArgs& p, int64_t e, const uint16_t* list,
+                                         int count, int s0, int s1,
+                                         f32x4_t (&red)[W::NW][2 * W::NF][64]) {
+  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U1 : W::U1 / 2, CW = 16 * NF;
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int groups = static_cast<int>((p.H + W::KS * NW * U - 1) / (W::KS * NW * U));
+  typename W::Strip sg, su;
+  auto at_strip = [&](int s) {
+    sg = W::strip(p.w1, p.w1s, e, p.H, 2 * p.I, 0, static_cast<int64_t>(s) * CW, p.I);
+    su = W::strip(p.w1, p.w1s, e, p.H, 2 * p.I, p.I, static_cast<int64_t>(s) * CW, p.I);
+  };
+  auto step = [&](int grp, int u) { return static_cast<int64_t>((grp * NW + wave) * U + u); };
+  typename W::template Group<U> wg, wu;
+  at_strip(s0);
+  wg.scales(sg, step(0, 0));
+  wu.scales(su, step(0, 0));
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    wg.load(sg, step(0, u), u);
+    wu.load(su, step(0, u), u);
+  }
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(reinterpret_cast<const char*>(p.x));
   uint32_t xr[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int r = 16 * i + (lane & 15);
-    xr[i] = static_cast<uint32_t>(list[r < count ? r : count - 1] / p.K * p.H * 2);
+    xr[i] = r < count ? static_cast<uint32_t>(list[r] / p.K * p.H * 2) : kOffNone;
   }
-  f32x4_t ag[NF][MT], au[NF][MT];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < MT; ++i) ag[f][i] = au[f][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int64_t steps = (p.H + W::KS - 1) / W::KS;
-  for (int64_t s0 = wave; s0 < steps; s0 += NW * U) {
-    W wg[U], wu[U];
-    u32x4_t a[U][W::KT][MT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t s = s0 + u * NW;
-      wg[u].load(sg, s);
-      wu[u].load(su, s);
-    }
+  u32x4_t a[U][W::KT][MT];
+  auto load_rows = [&](int grp) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < W::KT; ++t) {
-        const int64_t k = W::k0(s0 + u * NW, t, g);
+        const int64_t k = W::k0(step(grp, u), t, g);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
           a[u][t][i] = __builtin_amdgcn_raw_buffer_load_b128(
               rx, k < p.H ? xr[i] + static_cast<uint32_t>(2 * k) : kOffNone, 0, 0);
       }
+  };
+  load_rows(0);
+  for (int s = s0; s < s1; ++s) {
+    f32x4_t ag[NF][MT], au[NF][MT];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      sfor<W::KT>([&](auto Tc) {
-        constexpr int t = decltype(Tc)::value;
+    for (int f = 0; f < NF; ++f)
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          const bf16x8_t bg = wg[u].template frag<t>(f), bu = wu[u].template frag<t>(f);
+      for (int i = 0; i < MT; ++i) ag[f][i] = au[f][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int grp = 0; grp < groups; ++grp) {
+      const bool turn = grp + 1 == groups;
+      const int ng = turn ? 0 : grp + 1;
+      const bool more = !turn || s + 1 < s1;
+      if (turn && more) at_strip(s + 1);
+      wg.take();
+      wu.take();
+      if (more) {
+        wg.scales(sg, step(ng, 0));
+        wu.scales(su, step(ng, 0));
+      }
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            ag[f][i] = mfma_bf16(bit_cast<bf16x8_t>(a[u][t][i]), bg, ag[f][i]);
-            au[f][i] = mfma_bf16(bit_cast<bf16x8_t>(a[u][t][i]), bu, au[f][i]);
+      for (int u = 0; u < U; ++u) {
+        sfor<W::KT>([&](auto Tc) {
+          constexpr int t = decltype(Tc)::value;
+#pragma unroll
+          for (int f = 0; f < NF; ++f) {
+            const bf16x8_t bg = wg.template frag<t>(u, f), bu = wu.template frag<t>(u, f);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              ag[f][i] = mfma_bf16(bit_cast<bf16x8_t>(a[u][t][i]), bg, ag[f][i]);
+              au[f][i] = mfma_bf16(bit_cast<bf16x8_t>(a[u][t][i]), bu, au[f][i]);
+            }
           }
+        });
+        if (more) {
+          wg.load(sg, step(ng, u), u);
+          wu.load(su, step(ng, u), u);
         }
-      });
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    if (i) __syncthreads();
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      red[wave][f][lane] = ag[f][i];
-      red[wave][NF + f][lane] = au[f][i];
+      }
+      if (more && groups > 1) load_rows(ng);
     }
-    __syncthreads();
-    const int rows = count - 16 * i < 16 ? count - 16 * i : 16;
-    for (int q = threadIdx.x; q < rows * (16 * NF); q += NW * 64) {
-      const int m = q / (16 * NF), c = q - m * (16 * NF);
-      const int f = W::frag_of(c), n = W::lane_of(c);
-      if (c0 + c >= p.I) continue;
-      const float gate = tile_sum<NW>(red, f, m, n), up = tile_sum<NW>(red, NF + f, m, n);
-      const float h = gate / (1.f + __expf(-gate)) * up;
-      const uint16_t hi = f32_to_bf16_bits(h);
-      const float hf = bf16_bits_to_f32(hi);
-      // (an infinite h has no rest)
-      const float lo = __builtin_fabsf(hf) < __builtin_inff() ? h - hf : 0.f;
-      const int64_t at = static_cast<int64_t>(list[16 * i + m]) * p.I + c0 + c;
-      p.h_hi[at] = hi;
-      p.h_lo[at] = f32_to_bf16_bits(lo);
+    const int64_t c0 = static_cast<int64_t>(s) * CW;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        red[wave][f][lane] = ag[f][i];
+        red[wave][NF + f][lane] = au[f][i];
+      }
+      lds_barrier();
+      const int rows = count - 16 * i < 16 ? count - 16 * i : 16;
+      for (int q = threadIdx.x; q < rows * CW; q += NW * 64) {
+        const int m = q / CW, c = q - m * CW;
+        const int f = W::frag_of(c), n = W::lane_of(c);
+        if (c0 + c >= p.I) continue;
+        const float gate = tile_sum<NW>(red, f, m, n), up = tile_sum<NW>(red, NF + f, m, n);
+        const float h = gate / (1.f + __expf(-gate)) * up;
+        const uint16_t hi = f32_to_bf16_bits(h);
+        const float hf = bf16_bits_to_f32(hi);
+        // (an infinite h has no rest)
+        const float lo = __builtin_fabsf(hf) < __builtin_inff() ? h - hf : 0.f;
+        const int64_t at = static_cast<int64_t>(list[16 * i + m]) * p.I + c0 + c;
+        p.h_hi[at] = hi;
+        p.h_lo[at] = f32_to_bf16_bits(lo);
+      }
+      lds_barrier();
     }
   }
-  __syncthreads();
+}
+
+// Strips of a kernel's workgroup: `per` neighbouring ones.
+struct Strips {
+  int s0, s1;
+};
+__device__ __forceinline__ Strips my_strips(int strips, int per) {
+  const int s0 = blockIdx.x * per;
+  return {s0, s0 + per < strips ? s0 + per : strips};
 }
 
 // MANY: more than 16 tokens, so that an expert may have more than 16 slots of
 // different tokens; they are then taken 32 at a time.
 template <class W, bool MANY>
-__global__ __launch_bounds__(W::NW * 64) void tokens_fc1_kernel(TokArgs p) {
+__global__ __launch_bounds__(W::NW * 64, 2) void tokens_fc1_kernel(TokArgs p) {
   constexpr int NT = W::NW * 64;
   __shared__ PickMem mem;
   __shared__ f32x4_t red[W::NW][2 * W::NF][64];
-  if (blockIdx.y == 0) {  // a row of workgroups ahead of the experts': the plan
-    if (blockIdx.x == 0) write_plan<NT>(p, gridDim.y - 1);
+  if (blockIdx.y == 0) {  // a row of workgroups ahead of the experts': what fc2 needs
+    if (blockIdx.x == 0) write_plan<NT>(p, p.TK < p.El ? p.TK : p.El);
+    for (int t = blockIdx.x; t < p.T; t += gridDim.x) count_slots<NT>(p, t);
     return;
   }
   const Expert ex = pick_expert<NT>(p, blockIdx.y - 1, mem);
   if (ex.e < 0) return;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * (16 * W::NF);
-  const auto sg = W::strip(p.w1, p.w1s, ex.e, p.H, 2 * p.I, 0, c0, p.I);
-  const auto su = W::strip(p.w1, p.w1s, ex.e, p.H, 2 * p.I, p.I, c0, p.I);
+  const Strips st = my_strips(p.strips1, p.per1);
   for (int b = 0; b < ex.count;) {
     const int left = ex.count - b;
     if (MANY && left > 16) {
-      fc1_rows<W, kTokMany>(p, mem.list + b, left < 16 * kTokMany ? left : 16 * kTokMany, sg, su,
-                            c0, red);
+      fc1_rows<W, kTokMany>(p, ex.e, mem.list + b, left < 16 * kTokMany ? left : 16 * kTokMany,
+                            st.s0, st.s1, red);
       b += 16 * kTokMany;
     } else {
-      fc1_rows<W, 1>(p, mem.list + b, left < 16 ? left : 16, sg, su, c0, red);
+      fc1_rows<W, 1>(p, ex.e, mem.list + b, left < 16 ? left : 16, st.s0, st.s1, red);
       b += 16;
     }
   }
@@ -432,36 +504,39 @@ __global__ __launch_bounds__(W::NW * 64) void tokens_fc1_kernel(TokArgs p) {
 // ----------------------------------------------------------------------- fc2
 
 template <class W, int MT>
-__device__ __forceinline__ void fc2_rows(const TokArgs& p, const uint16_t* list, int count,
-                                         const typename W::Strip& sw, int64_t c0,
+__device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint16_t* list,
+                                         int count, int s0, int s1,
                                          f32x4_t (&red)[W::NW][W::NF][64]) {
-  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U : 1;
+  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U2 : W::U2 / 2, CW = 16 * NF;
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int groups = static_cast<int>((p.I + W::KS * NW * U - 1) / (W::KS * NW * U));
+  typename W::Strip sw;
+  auto at_strip = [&](int s) {
+    sw = W::strip(p.w2, p.w2s, e, p.I, p.H, 0, static_cast<int64_t>(s) * CW, p.H);
+  };
+  auto step = [&](int grp, int u) { return static_cast<int64_t>((grp * NW + wave) * U + u); };
+  typename W::template Group<U> w;
+  at_strip(s0);
+  w.scales(sw, step(0, 0));
+#pragma unroll
+  for (int u = 0; u < U; ++u) w.load(sw, step(0, u), u);
   const __amdgpu_buffer_rsrc_t rhi = make_rsrc(reinterpret_cast<const char*>(p.h_hi));
   const __amdgpu_buffer_rsrc_t rlo = make_rsrc(reinterpret_cast<const char*>(p.h_lo));
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(reinterpret_cast<const char*>(p.y));
   uint32_t hr[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int r = 16 * i + (lane & 15);
-    hr[i] = static_cast<uint32_t>(list[r < count ? r : count - 1] * p.I * 2);
+    hr[i] = r < count ? static_cast<uint32_t>(list[r] * p.I * 2) : kOffNone;
   }
-  f32x4_t acc[NF][MT];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[f][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int64_t steps = (p.I + W::KS - 1) / W::KS;
-  for (int64_t s0 = wave; s0 < steps; s0 += NW * U) {
-    W w[U];
-    u32x4_t hi[U][W::KT][MT], lo[U][W::KT][MT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) w[u].load(sw, s0 + u * NW);
+  u32x4_t hi[U][W::KT][MT], lo[U][W::KT][MT];
+  auto load_rows = [&](int grp) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < W::KT; ++t) {
-        const int64_t k = W::k0(s0 + u * NW, t, g);
+        const int64_t k = W::k0(step(grp, u), t, g);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           const uint32_t off = k < p.I ? hr[i] + static_cast<uint32_t>(2 * k) : kOffNone;
@@ -469,117 +544,145 @@ __device__ __forceinline__ void fc2_rows(const TokArgs& p, const uint16_t* list,
           lo[u][t][i] = __builtin_amdgcn_raw_buffer_load_b128(rlo, off, 0, 0);
         }
       }
+  };
+  load_rows(0);
+  for (int s = s0; s < s1; ++s) {
+    f32x4_t acc[NF][MT];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      sfor<W::KT>([&](auto Tc) {
-        constexpr int t = decltype(Tc)::value;
+    for (int f = 0; f < NF; ++f)
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          const bf16x8_t b = w[u].template frag<t>(f);
+      for (int i = 0; i < MT; ++i) acc[f][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int grp = 0; grp < groups; ++grp) {
+      const bool turn = grp + 1 == groups;
+      const int ng = turn ? 0 : grp + 1;
+      const bool more = !turn || s + 1 < s1;
+      if (turn && more) at_strip(s + 1);
+      w.take();
+      if (more) w.scales(sw, step(ng, 0));
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(hi[u][t][i]), b, acc[f][i]);
-            acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(lo[u][t][i]), b, acc[f][i]);
+      for (int u = 0; u < U; ++u) {
+        sfor<W::KT>([&](auto Tc) {
+          constexpr int t = decltype(Tc)::value;
+#pragma unroll
+          for (int f = 0; f < NF; ++f) {
+            const bf16x8_t b = w.template frag<t>(u, f);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(hi[u][t][i]), b, acc[f][i]);
+              acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(lo[u][t][i]), b, acc[f][i]);
+            }
           }
-        }
-      });
-  }
-  const __amdgpu_buffer_rsrc_t ry = make_rsrc(reinterpret_cast<const char*>(p.y));
+        });
+        if (more) w.load(sw, step(ng, u), u);
+      }
+      if (more && groups > 1) load_rows(ng);
+    }
+    const int64_t c0 = static_cast<int64_t>(s) * CW;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    if (i) __syncthreads();
+    for (int i = 0; i < MT; ++i) {
 #pragma unroll
-    for (int f = 0; f < NF; ++f) red[wave][f][lane] = acc[f][i];
-    __syncthreads();
-    const int rows = count - 16 * i < 16 ? count - 16 * i : 16;
-    for (int q = threadIdx.x; q < rows * (16 * NF); q += NW * 64) {
-      const int m = q / (16 * NF), c = q - m * (16 * NF);
-      if (c0 + c >= p.H) continue;
-      const float v = tile_sum<NW>(red, W::frag_of(c), m, W::lane_of(c));
-      const int64_t at = static_cast<int64_t>(list[16 * i + m]) * p.H + c0 + c;
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ry, static_cast<int>(at * 4), 0,
-                                            kCpolAgent);
+      for (int f = 0; f < NF; ++f) red[wave][f][lane] = acc[f][i];
+      lds_barrier();
+      const int rows = count - 16 * i < 16 ? count - 16 * i : 16;
+      for (int q = threadIdx.x; q < rows * CW; q += NW * 64) {
+        const int m = q / CW, c = q - m * CW;
+        if (c0 + c >= p.H) continue;
+        const float v = tile_sum<NW>(red, W::frag_of(c), m, W::lane_of(c));
+        const int64_t at = static_cast<int64_t>(list[16 * i + m]) * p.H + c0 + c;
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ry, static_cast<int>(at * 4), 0,
+                                              kCpolAgent);
+      }
+      lds_barrier();
     }
   }
-  __syncthreads();
 }
 
-// out[t] = sum over the local slots of t, in slot order, of probs * y: columns
-// c0 .. c0 + cw of every token.
-template <int NT>
-__device__ __forceinline__ void sum_slots(const TokArgs& p, int64_t c0, int cw) {
+// out[t] = sum over the local slots of t, in slot order, of probs * y: four
+// columns from c on.
+__device__ __forceinline__ void sum_slots(const TokArgs& p, int t, int64_t c) {
   const __amdgpu_buffer_rsrc_t ry = make_rsrc(reinterpret_cast<const char*>(p.y));
-  const int q4 = cw / 4;
-  for (int q = threadIdx.x; q < p.T * q4; q += NT) {
-    const int t = q / q4;
-    const int64_t c = c0 + 4 * (q - t * q4);
-    if (c >= p.H) continue;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k0 = 0; k0 < p.K; k0 += 8) {  // eight slots' loads in flight
-      u32x4_t y[8];
-      float w[8];
-      bool in[8];
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < p.K; k0 += 8) {  // eight slots' loads in flight
+    u32x4_t y[8];
+    float w[8];
+    bool in[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int s = t * p.K + (k0 + j < p.K ? k0 + j : p.K - 1);
-        in[j] = k0 + j < p.K && local_id(p, s) >= 0;
-        w[j] = p.probs[s];
-        y[j] = __builtin_amdgcn_raw_buffer_load_b128(
-            ry, in[j] ? static_cast<uint32_t>((static_cast<int64_t>(s) * p.H + c) * 4) : kOffNone, 0,
-            kCpolAgent);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (in[j]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(w[j], __uint_as_float(y[j][i]), v[i]);
-        }
+    for (int j = 0; j < 8; ++j) {
+      const int s = t * p.K + (k0 + j < p.K ? k0 + j : p.K - 1);
+      in[j] = k0 + j < p.K && local_id(p, s) >= 0;
+      w[j] = p.probs[s];
+      y[j] = __builtin_amdgcn_raw_buffer_load_b128(
+          ry, in[j] ? static_cast<uint32_t>((static_cast<int64_t>(s) * p.H + c) * 4) : kOffNone, 0,
+          kCpolAgent);
     }
-    *reinterpret_cast<u32x2_t*>(p.out + static_cast<int64_t>(t) * p.H + c) = pack4<Out::BF16>(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (in[j]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(w[j], __uint_as_float(y[j][i]), v[i]);
+      }
   }
+  *reinterpret_cast<u32x2_t*>(p.out + static_cast<int64_t>(t) * p.H + c) = pack4<Out::BF16>(v);
 }
+
+constexpr int kTokDone = 2048;  // finished (strip, token) pairs held at a time
 
 template <class W, bool MANY>
-__global__ __launch_bounds__(W::NW * 64) void tokens_fc2_kernel(TokArgs p) {
+__global__ __launch_bounds__(W::NW * 64, 2) void tokens_fc2_kernel(TokArgs p) {
   constexpr int NT = W::NW * 64, CW = 16 * W::NF;
   __shared__ f32x4_t red[W::NW][W::NF][64];
-  __shared__ int last;
+  __shared__ uint16_t done[kTokDone];  // strip (from the workgroup's first) * 256 + token
+  __shared__ int ndone;
   const i32x4_t plan = p.plan[blockIdx.y];
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * CW;
-  const int count = plan[1], named = plan[3];
-  if (plan[0] < 0) {
-    // no slot is local: the output is zeros
-    if (named == 0 && blockIdx.y == 0) sum_slots<NT>(p, c0, CW);
-    return;
-  }
-  const auto sw = W::strip(p.w2, p.w2s, plan[0], p.I, p.H, 0, c0, p.H);
+  const int count = plan[1];
+  const Strips st = my_strips(p.strips2, p.per2);
+  if (plan[0] < 0) return;
   const uint16_t* list = p.list + plan[2];
   for (int b = 0; b < count;) {
     const int left = count - b;
     if (MANY && left > 16) {
-      fc2_rows<W, kTokMany>(p, list + b, left < 16 * kTokMany ? left : 16 * kTokMany, sw, c0, red);
+      fc2_rows<W, kTokMany>(p, plan[0], list + b, left < 16 * kTokMany ? left : 16 * kTokMany,
+                            st.s0, st.s1, red);
       b += 16 * kTokMany;
     } else {
-      fc2_rows<W, 1>(p, list + b, left < 16 ? left : 16, sw, c0, red);
+      fc2_rows<W, 1>(p, plan[0], list + b, left < 16 ? left : 16, st.s0, st.s1, red);
       b += 16;
     }
   }
+  // The workgroup that brings the last y of a token's strip adds the token up.
   // y was written through to memory and is read from there: once the stores
   // are done (the wait), no cache needs a write-back or an invalidation, which
-  // would cost the other workgroups their weights
+  // would cost the other workgroups their weights.
+  if (threadIdx.x == 0) ndone = 0;
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (threadIdx.x == 0)
-    last = __hip_atomic_fetch_add(&p.arrived[blockIdx.x], 1u, __ATOMIC_RELAXED,
-                                  __HIP_MEMORY_SCOPE_AGENT) + 1 == static_cast<uint32_t>(named);
-  __syncthreads();
-  if (last) sum_slots<NT>(p, c0, CW);
+  const int most = count < p.T ? count : p.T;  // tokens that a strip can finish here
+  const int batch = kTokDone / most;
+  for (int s0 = st.s0; s0 < st.s1; s0 += batch) {
+    const int ns = s0 + batch < st.s1 ? batch : st.s1 - s0;
+    for (int q = threadIdx.x; q < ns * count; q += NT) {
+      const int s = q / count, t = list[q - s * count] / p.K;
+      if (__hip_atomic_fetch_add(&p.left[(s0 + s) * p.T + t], -1, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT) == 1)
+        done[atomicAdd(&ndone, 1)] = static_cast<uint16_t>((s0 - st.s0 + s) * 256 + t);
+    }
+    __syncthreads();
+    const int items = ndone * (CW / 4);
+    for (int q = threadIdx.x; q < items; q += NT) {
+      const int d = done[q / (CW / 4)];
+      const int64_t c = static_cast<int64_t>(st.s0 + (d >> 8)) * CW + 4 * (q % (CW / 4));
+      if (c < p.H) sum_slots(p, d & 255, c);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) ndone = 0;
+    __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------------ host side
 
 struct TokWorkspace {
-  size_t arrived, plan, list, h, y, bytes;
+  size_t left, plan, list, h, y, bytes;
 };
 
 static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -589,8 +692,8 @@ static bool tok_workspace(int64_t T, int K, int64_t H, int64_t I, TokWorkspace& 
   if (H < 8 || H > 65536 || I < 8 || I > 65536) return false;
   const int64_t TK = T * K;
   if (TK * H >= int64_t{1} << 28 || TK * I >= int64_t{1} << 28) return false;
-  w.arrived = 0;
-  w.plan = up256(static_cast<size_t>(tok_strips(H)) * 4);
+  w.left = 0;
+  w.plan = up256(static_cast<size_t>(tok_strips(H) * T) * 4);
   w.list = w.plan + up256(static_cast<size_t>(TK < kTokMaxExperts ? TK : kTokMaxExperts) * 16);
   w.h = w.list + up256(static_cast<size_t>(TK) * 2);
   w.y = w.h + up256(static_cast<size_t>(TK * I) * 2) * 2;
@@ -598,33 +701,40 @@ static bool tok_workspace(int64_t T, int K, int64_t H, int64_t I, TokWorkspace& 
   return true;
 }
 
-template <class W, bool MANY>
-static void launch_fc1(const TokArgs& a, int slots, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.I + 16 * W::NF - 1) / (16 * W::NF)), slots + 1);
-  hipLaunchKernelGGL((tokens_fc1_kernel<W, MANY>), grid, dim3(W::NW * 64), 0, s, a);
+// Strips a workgroup, so that about eight workgroups a CU remain.
+static int strips_per(int64_t strips, int64_t rows, int64_t cus) {
+  const int64_t per = strips * rows / (6 * cus);
+  return static_cast<int>(per < 1 ? 1 : per < kTokMaxPer ? per : kTokMaxPer);
 }
-template <class W, bool MANY>
-static void launch_fc2(const TokArgs& a, int slots, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.H + 16 * W::NF - 1) / (16 * W::NF)), slots);
-  hipLaunchKernelGGL((tokens_fc2_kernel<W, MANY>), grid, dim3(W::NW * 64), 0, s, a);
+
+template <class W1, class W2, bool MANY>
+static void launch_both(TokArgs a, int rows1, int rows2, int64_t cus, hipStream_t s) {
+  a.strips1 = static_cast<int>((a.I + 16 * W1::NF - 1) / (16 * W1::NF));
+  a.strips2 = static_cast<int>((a.H + 16 * W2::NF - 1) / (16 * W2::NF));
+  a.per1 = strips_per(a.strips1, rows1, cus);
+  a.per2 = strips_per(a.strips2, rows2, cus);
+  const dim3 grid1((a.strips1 + a.per1 - 1) / a.per1, rows1 + 1);
+  const dim3 grid2((a.strips2 + a.per2 - 1) / a.per2, rows2);
+  hipLaunchKernelGGL((tokens_fc1_kernel<W1, MANY>), grid1, dim3(W1::NW * 64), 0, s, a);
+  hipLaunchKernelGGL((tokens_fc2_kernel<W2, MANY>), grid2, dim3(W2::NW * 64), 0, s, a);
 }
 
 // Narrow strips where wide ones would not fill the CUs.
 template <bool MANY>
 static void launch_tokens(const TokArgs& a, bool mx4, hipStream_t s) {
   const int slots = a.TK < a.El ? a.TK : a.El;
+  const int rows1 = a.TK <= 64 ? slots : a.El;  // see pick_expert
   const int64_t cus = num_cus();
-  const bool wide1 = slots * ((a.I + 63) / 64) >= cus, wide2 = slots * ((a.H + 63) / 64) >= cus;
+  const bool wide1 = slots * ((a.I + 63) / 64) >= cus / 4, wide2 = slots * ((a.H + 63) / 64) >= cus / 4;
+  auto both = [&](auto w1, auto w2) {
+    launch_both<decltype(w1), decltype(w2), MANY>(a, rows1, slots, cus, s);
+  };
   if (mx4) {
-    if (wide1) launch_fc1<WMx4<2>, MANY>(a, slots, s);
-    else launch_fc1<WMx4<1>, MANY>(a, slots, s);
-    if (wide2) launch_fc2<WMx4<4>, MANY>(a, slots, s);
-    else launch_fc2<WMx4<1>, MANY>(a, slots, s);
+    if (wide1) wide2 ? both(WMx4<2>{}, WMx4<4>{}) : both(WMx4<2>{}, WMx4<1>{});
+    else wide2 ? both(WMx4<1>{}, WMx4<4>{}) : both(WMx4<1>{}, WMx4<1>{});
   } else {
-    if (wide1) launch_fc1<WBf16<4>, MANY>(a, slots, s);
-    else launch_fc1<WBf16<2>, MANY>(a, slots, s);
-    if (wide2) launch_fc2<WBf16<4>, MANY>(a, slots, s);
-    else launch_fc2<WBf16<2>, MANY>(a, slots, s);
+    if (wide1) wide2 ? both(WBf16<4>{}, WBf16<4>{}) : both(WBf16<4>{}, WBf16<2>{});
+    else wide2 ? both(WBf16<2>{}, WBf16<4>{}) : both(WBf16<2>{}, WBf16<2>{});
   }
 }
 
@@ -667,7 +777,7 @@ extern "C" int mc2_moe_tokens(const void* x, const int32_t* sel, const float* pr
   a.w2 = static_cast<const char*>(w2);
   a.w2s = static_cast<const char*>(w2_scale);
   a.out = static_cast<uint16_t*>(out);
-  a.arrived = reinterpret_cast<uint32_t*>(ws + w.arrived);
+  a.left = reinterpret_cast<int32_t*>(ws + w.left);
   a.plan = reinterpret_cast<i32x4_t*>(ws + w.plan);
   a.list = reinterpret_cast<uint16_t*>(ws + w.list);
   a.h_hi = reinterpret_cast<uint16_t*>(ws + w.h);

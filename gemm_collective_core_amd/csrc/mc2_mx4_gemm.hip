@@ -140,8 +140,8 @@ __global__ __launch_bounds__(TS::NT, TS::BM == 256 ? 1 : 2) void mx4_tile_kernel
 // A workgroup of NW waves computes MT x 16 rows by 16 columns: wave w sums the
 // 512-value chunks w, w + NW, ... of K, and the waves' sums are added in order
 // through LDS. A lane takes row (lane & 15) of A and of B and, of a chunk, the
-// 64 bytes of blocks 4 g .. 4 g + 3, g = lane >> 4: whole 256-byte pieces of
-// each row per wave, and the chunk's four scale bytes of a lane are one dword.
+// blocks 4 j + g, g = lane >> 4: a load is 64 contiguous bytes of 16 rows. The 16
+// scale bytes of a row's chunk are one load, from which a lane picks its own.
 // The weights are read once, straight into registers.
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
@@ -160,43 +160,41 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4Args p) {
   const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 16;
   const int64_t ld = p.nb * 16;
   const int64_t col = col0 + r < p.n ? col0 + r : p.n - 1;
-  const char* bc = p.B + col * ld + g * 64;
-  const char* bs = p.Bs + col * p.pitch + g * 4;
+  const char* bc = p.B + col * ld + g * 16;
+  const char* bs = p.Bs + col * p.pitch;
   const char* ac[MT];
   const char* as[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int64_t row = row0 + i * 16 + r < p.m ? row0 + i * 16 + r : p.m - 1;
-    ac[i] = p.A + row * ld + g * 64;
-    as[i] = p.As + row * p.pitch + g * 4;
+    ac[i] = p.A + row * ld + g * 16;
+    as[i] = p.As + row * p.pitch;
   }
   f32x4_t acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int64_t chunks = p.pitch / 16;
   for (int64_t c = wave; c < chunks; c += NW) {
-    const int64_t left = p.nb - c * 16 - g * 4;  // blocks of this lane's four that exist
-    u32x4_t vb[4], va[MT][4];
-    const int sb = *reinterpret_cast<const int*>(bs + c * 16);
-    int sa[MT];
+    const int64_t left = p.nb - c * 16 - g;  // block 4 j of the lane's exists where 4 j < left
+    u32x4_t vb[4], va[MT][4], sa[MT];
+    const u32x4_t sb = *reinterpret_cast<const u32x4_t*>(bs + c * 16);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      vb[j] = j < left ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(bc + c * 256 + j * 16))
-                       : zero_v4();
+      vb[j] = 4 * j < left ? *reinterpret_cast<const u32x4_t*>(bc + c * 256 + j * 64) : zero_v4();
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      sa[i] = *reinterpret_cast<const int*>(as[i] + c * 16);
+      sa[i] = *reinterpret_cast<const u32x4_t*>(as[i] + c * 16);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        va[i][j] = j < left ? *reinterpret_cast<const u32x4_t*>(ac[i] + c * 256 + j * 16) : zero_v4();
+        va[i][j] = 4 * j < left ? *reinterpret_cast<const u32x4_t*>(ac[i] + c * 256 + j * 64) : zero_v4();
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx4_op(vb[0]), mx4_op(va[i][0]), acc[i], 4, 4, 0, sb, 0, sa[i]);
-      acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx4_op(vb[1]), mx4_op(va[i][1]), acc[i], 4, 4, 1, sb, 1, sa[i]);
-      acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx4_op(vb[2]), mx4_op(va[i][2]), acc[i], 4, 4, 2, sb, 2, sa[i]);
-      acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx4_op(vb[3]), mx4_op(va[i][3]), acc[i], 4, 4, 3, sb, 3, sa[i]);
-    }
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            mx4_op(vb[j]), mx4_op(va[i][j]), acc[i], 4, 4, 0, static_cast<int>(sb[j] >> (8 * g)), 0,
+            static_cast<int>(sa[i][j] >> (8 * g)));
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
