@@ -25,6 +25,7 @@ struct Mx4Args {
   int tiles_n, tiles_m1, tiles_m0;  // tile columns, tile rows of a long and a short piece
   int tiles_per_chunk;
   int round;
+  int n_full;  // work units below are whole tiles, the rest half tiles (two a tile)
   uint32_t* flags;
   uint32_t* counters;
   uint32_t epoch;
@@ -67,16 +68,18 @@ __device__ __forceinline__ Mx4Pos mx4_pos(const Mx4Args& p, int tile, int bm, in
   return q;
 }
 
-// Counts the tile as done; the last of a segment raises its flag (the protocol
-// of the rank-chunked GEMM: a release per tile, one acquire per segment).
-__device__ __forceinline__ void mx4_count(const Mx4Args& p, int seg, int seg_tiles) {
+// Counts `weight` half tiles as done; the last of a segment raises its flag (the
+// protocol of the rank-chunked GEMM: a release per tile, one acquire per
+// segment).
+__device__ __forceinline__ void mx4_count(const Mx4Args& p, int seg, int seg_tiles,
+                                          uint32_t weight) {
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
   if (threadIdx.x == 0) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    const uint32_t prev = __hip_atomic_fetch_add(&p.counters[seg], 1u, __ATOMIC_RELAXED,
+    const uint32_t prev = __hip_atomic_fetch_add(&p.counters[seg], weight, __ATOMIC_RELAXED,
                                                  __HIP_MEMORY_SCOPE_AGENT);
-    if (prev + 1 == static_cast<uint32_t>(seg_tiles)) {
+    if (prev + weight == 2u * static_cast<uint32_t>(seg_tiles)) {
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
       __hip_atomic_store(&p.counters[seg], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __hip_atomic_store(&p.flags[seg], p.epoch, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_SYSTEM);
@@ -84,14 +87,17 @@ __device__ __forceinline__ void mx4_count(const Mx4Args& p, int seg, int seg_til
   }
 }
 
+template <class TS>
+constexpr int mx4_smem() {
+  constexpr int staged = TS::BM * (TS::BN * 2 + 16);
+  return TS::kLoopBytes > staged ? TS::kLoopBytes : staged;
+}
+
+// The tile at t, which has rows.
 template <class TS, Out O, bool KTAIL>
-__global__ __launch_bounds__(TS::NT, TS::BM == 256 ? 1 : 2) void mx4_tile_kernel(Mx4Args p) {
+__device__ __forceinline__ void mx4_tile(const Mx4Args& p, lds_t* smem, const Mx4Pos& t) {
   constexpr int OS = OutInfo<O>::bytes;
   constexpr int pitch = TS::BN * 2 + 16;  // staged 16-bit rows
-  constexpr int kSmem = TS::kLoopBytes > TS::BM * pitch ? TS::kLoopBytes : TS::BM * pitch;
-  __shared__ __attribute__((aligned(16))) char smem_raw[kSmem];
-  lds_t* smem = (lds_t*)smem_raw;
-  const Mx4Pos t = mx4_pos(p, xcd_tile(blockIdx.x, p.round, gridDim.x), TS::BM, TS::BN);
   const int64_t ld = p.nb * 16;
   const MxSide a{p.A + t.row0 * ld, p.As + t.row0 * p.pitch, t.row_end - 1 - t.row0};
   const MxSide b{p.B + t.col0 * ld, p.Bs + t.col0 * p.pitch, p.n - 1 - t.col0};
@@ -132,12 +138,38 @@ __global__ __launch_bounds__(TS::NT, TS::BM == 256 ? 1 : 2) void mx4_tile_kernel
     store_staged<TS::NT>(smem, pitch, TS::BN * 2, TS::BM, p.out + t.row0 * p.ldo, p.ldo, nrows,
                          t.col0 * 2, p.n * 2, p.store_wt != 0);
   }
-  if (p.flags) mx4_count(p, t.seg, t.seg_tiles);
+}
+
+using MxL = MxTile<256, 256, 1>;
+using MxH = MxTile<128, 256, 2>;  // half a large tile
+using MxS = MxTile<128, 128, 2>;
+
+// One workgroup per work unit: a tile, or of a last round of 256 x 256 tiles
+// that would leave half of the CUs idle, the upper or lower half of one.
+template <class TS, Out O, bool KTAIL>
+__global__ __launch_bounds__(TS::NT, TS::BM == 256 ? 1 : 2) void mx4_tile_kernel(Mx4Args p) {
+  __shared__ __attribute__((aligned(16))) char smem_raw[mx4_smem<TS>()];
+  lds_t* smem = (lds_t*)smem_raw;
+  const int u = xcd_tile(blockIdx.x, p.round, gridDim.x);
+  Mx4Pos t;
+  if (TS::BM == 256 && u >= p.n_full) {
+    if constexpr (TS::BM == 256) {
+      const int v = u - p.n_full;
+      t = mx4_pos(p, p.n_full + (v >> 1), TS::BM, TS::BN);
+      t.row0 += (v & 1) * MxH::BM;
+      if (t.row0 < t.row_end) mx4_tile<MxH, O, KTAIL>(p, smem, t);
+      if (p.flags) mx4_count(p, t.seg, t.seg_tiles, 1u);
+    }
+    return;
+  }
+  t = mx4_pos(p, u, TS::BM, TS::BN);
+  mx4_tile<TS, O, KTAIL>(p, smem, t);
+  if (p.flags) mx4_count(p, t.seg, t.seg_tiles, 2u);
 }
 
 // ------------------------------------------------------------------- few rows
 //
-// A workgroup of NW waves computes MT x 16 rows by 16 columns: wave w sums the
+// A workgroup of NW waves computes MT x 16 rows by NT x 16 columns: wave w sums the
 // 512-value chunks w, w + NW, ... of K, and the waves' sums are added in order
 // through LDS. A lane takes row (lane & 15) of A and of B and, of a chunk, the
 // blocks 4 j + g, g = lane >> 4: a load is 64 contiguous bytes of 16 rows. The 16
@@ -150,18 +182,23 @@ __device__ __forceinline__ i32x8_t mx4_op(u32x4_t v) {
                  static_cast<int>(v[3]), 0, 0, 0, 0};
 }
 
-template <int MT, int NW, Out O>
+template <int MT, int NT, int NW, Out O>
 __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4Args p) {
   constexpr int OS = OutInfo<O>::bytes;
-  __shared__ f32x4_t red[NW][MT][64];
+  __shared__ f32x4_t red[NW][NT][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
   const int64_t row0 = static_cast<int64_t>(blockIdx.y) * (MT * 16);
-  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * (NT * 16);
   const int64_t ld = p.nb * 16;
-  const int64_t col = col0 + r < p.n ? col0 + r : p.n - 1;
-  const char* bc = p.B + col * ld + g * 16;
-  const char* bs = p.Bs + col * p.pitch;
+  const char* bc[NT];
+  const char* bs[NT];
+#pragma unroll
+  for (int f = 0; f < NT; ++f) {
+    const int64_t col = col0 + f * 16 + r < p.n ? col0 + f * 16 + r : p.n - 1;
+    bc[f] = p.B + col * ld + g * 16;
+    bs[f] = p.Bs + col * p.pitch;
+  }
   const char* ac[MT];
   const char* as[MT];
 #pragma unroll
@@ -170,17 +207,22 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4Args p) {
     ac[i] = p.A + row * ld + g * 16;
     as[i] = p.As + row * p.pitch;
   }
-  f32x4_t acc[MT];
+  f32x4_t acc[NT][MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int f = 0; f < NT; ++f)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[f][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int64_t chunks = p.pitch / 16;
   for (int64_t c = wave; c < chunks; c += NW) {
     const int64_t left = p.nb - c * 16 - g;  // block 4 j of the lane's exists where 4 j < left
-    u32x4_t vb[4], va[MT][4], sa[MT];
-    const u32x4_t sb = *reinterpret_cast<const u32x4_t*>(bs + c * 16);
+    u32x4_t vb[NT][4], sb[NT], va[MT][4], sa[MT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      vb[j] = 4 * j < left ? *reinterpret_cast<const u32x4_t*>(bc + c * 256 + j * 64) : zero_v4();
+    for (int f = 0; f < NT; ++f) {
+      sb[f] = *reinterpret_cast<const u32x4_t*>(bs[f] + c * 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        vb[f][j] = 4 * j < left ? *reinterpret_cast<const u32x4_t*>(bc[f] + c * 256 + j * 64) : zero_v4();
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       sa[i] = *reinterpret_cast<const u32x4_t*>(as[i] + c * 16);
@@ -191,21 +233,25 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4Args p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            mx4_op(vb[j]), mx4_op(va[i][j]), acc[i], 4, 4, 0, static_cast<int>(sb[j] >> (8 * g)), 0,
-            static_cast<int>(sa[i][j] >> (8 * g)));
+      for (int f = 0; f < NT; ++f)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          acc[f][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              mx4_op(vb[f][j]), mx4_op(va[i][j]), acc[f][i], 4, 4, 0,
+              static_cast<int>(sb[f][j] >> (8 * g)), 0, static_cast<int>(sa[i][j] >> (8 * g)));
   }
 #pragma unroll
-  for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
+  for (int f = 0; f < NT; ++f)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) red[wave][f][i][lane] = acc[f][i];
   __syncthreads();
   // B was the first operand: a lane holds row (lane & 15), columns 4 g .. + 3
-  for (int q = threadIdx.x; q < MT * 64; q += NW * 64) {
-    const int i = q >> 6, l = q & 63;
-    f32x4_t s = red[0][i][l];
+  for (int q = threadIdx.x; q < NT * MT * 64; q += NW * 64) {
+    const int f = q / (MT * 64), i = (q >> 6) % MT, l = q & 63;
+    f32x4_t s = red[0][f][i][l];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) s += red[w][i][l];
-    const int64_t row = row0 + i * 16 + (l & 15), cc = col0 + 4 * (l >> 4);
+    for (int w = 1; w < NW; ++w) s += red[w][f][i][l];
+    const int64_t row = row0 + i * 16 + (l & 15), cc = col0 + f * 16 + 4 * (l >> 4);
     if (row < p.m && cc < p.n) {
       float v[4];
 #pragma unroll
@@ -220,15 +266,33 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4Args p) {
 
 // ------------------------------------------------------------------ host side
 
+template <int MT, int NT, Out O>
+static void launch_rows_of(const Mx4Args& a, hipStream_t s) {
+  constexpr int NW = 8;
+  const dim3 grid(static_cast<unsigned>((a.n + 16 * NT - 1) / (16 * NT)),
+                  static_cast<unsigned>((a.m + 16 * MT - 1) / (16 * MT)));
+  hipLaunchKernelGGL((mx4_rows_kernel<MT, NT, NW, O>), grid, dim3(NW * 64), 0, s, a);
+}
+// Workgroups of 32 rows by 16 * nt columns.
+static int64_t rows_groups(const Mx4Args& a, int64_t nt) {
+  return (a.m + 31) / 32 * ((a.n + 16 * nt - 1) / (16 * nt));
+}
+
+// The narrowest tile whose workgroups find a CU each, else the widest (us on the
+// GPU at 32 x 8192 x 8192, 16 / 32 / 64 columns, 512 / 256 / 128 workgroups: 17.2
+// / 13.9 / 17.3; at 64 x 8192 x 3584, 448 / 224 / 112: 16.9 / 12.6 / 17.4; for up
+// to 16 rows, which 16-row tiles serve, at 16 x 8192 x 8192: 12.4 / 11.4 / 14.7).
 template <Out O>
 static hipError_t launch_rows(const Mx4Args& a, hipStream_t s) {
-  const int mt = a.m <= 16 ? 1 : a.m <= 32 ? 2 : 4;
-  const dim3 grid(static_cast<unsigned>((a.n + 15) / 16),
-                  static_cast<unsigned>((a.m + 16 * mt - 1) / (16 * mt)));
-  constexpr int NW = 8;
-  if (mt == 1) hipLaunchKernelGGL((mx4_rows_kernel<1, NW, O>), grid, dim3(NW * 64), 0, s, a);
-  else if (mt == 2) hipLaunchKernelGGL((mx4_rows_kernel<2, NW, O>), grid, dim3(NW * 64), 0, s, a);
-  else hipLaunchKernelGGL((mx4_rows_kernel<4, NW, O>), grid, dim3(NW * 64), 0, s, a);
+  const int64_t cus = num_cus();
+  if (a.m <= 16) {
+    if (rows_groups(a, 1) <= cus) launch_rows_of<1, 1, O>(a, s);
+    else launch_rows_of<1, 2, O>(a, s);
+  } else {
+    if (rows_groups(a, 1) <= cus) launch_rows_of<2, 1, O>(a, s);
+    else if (rows_groups(a, 2) <= cus) launch_rows_of<2, 2, O>(a, s);
+    else launch_rows_of<2, 4, O>(a, s);
+  }
   return hipGetLastError();
 }
 
@@ -241,23 +305,28 @@ static hipError_t launch_tiles(const Mx4Args& a, unsigned blocks, hipStream_t s)
   return hipGetLastError();
 }
 
-using MxL = MxTile<256, 256, 1>;
-using MxS = MxTile<128, 128, 2>;
-
 // Tiles of one chunk for tiles of bm rows and tn tile columns.
 static int64_t mx4_chunk_tiles(const Mx4Args& a, int bm, int64_t tn) {
   return (a.sr * ((a.sq + bm) / bm) + (a.sub - a.sr) * ((a.sq + bm - 1) / bm)) * tn;
 }
 
-// Rows up to which a call without flags takes mx4_rows_kernel.
-constexpr int64_t kMx4FewRows = 64;
+// A call without flags takes mx4_rows_kernel for up to 64 rows, and for more
+// where its widest tiles find a CU each (128 x 8192 x 3584: 17.4 us against 21.0
+// with 128 x 128 tiles; 256 x 2048 x 1024: 5.2 against 7.6; past one round the
+// tiles win: 256 x 8192 x 3584 32 against 21).
+static bool few_rows(const Mx4Args& a) {
+  return !a.flags && (a.m <= 64 || rows_groups(a, 4) <= num_cus());
+}
 
 template <Out O>
 static int run_mx4(Mx4Args a, hipStream_t s) {
-  if (!a.flags && a.m <= kMx4FewRows) return launch_rows<O>(a, s) == hipSuccess ? MC2_OK : MC2_ERR_HIP;
+  if (few_rows(a)) return launch_rows<O>(a, s) == hipSuccess ? MC2_OK : MC2_ERR_HIP;
   const int64_t cus = num_cus();
   const int64_t tl = mx4_chunk_tiles(a, 256, (a.n + 255) / 256) * a.world;
-  const bool large = tl >= cus / 2;
+  // 128 x 128 tiles while they find a CU each, then 256 x 256 (us, small against
+  // large: 1024 x 4096 x 4096, 64 large tiles, 15.2 / 18.4; 1280 x 4096 x 4096, 80,
+  // 22.0 / 18.8; 1024 x 8192 x 5120, 80, 38.6 / 33.6)
+  const bool large = 4 * tl > cus;
   const int bm = large ? 256 : 128;
   a.tiles_n = static_cast<int>((a.n + bm - 1) / bm);
   const int64_t m1 = (a.sq + bm) / bm, m0 = (a.sq + bm - 1) / bm;
@@ -267,7 +336,13 @@ static int run_mx4(Mx4Args a, hipStream_t s) {
   a.tiles_m0 = static_cast<int>(m0);
   a.tiles_per_chunk = static_cast<int>(per);
   a.round = static_cast<int>(cus / 8 * 8) * (large ? 1 : 2);
-  const unsigned blocks = static_cast<unsigned>(per * a.world);
+  // A last (or only) round of 256 x 256 tiles that is at most half full runs as
+  // half tiles (us, whole against halves: 16384 x 8192 x 3584 in 8 chunks 242 /
+  // 234; 8192 x 4096 x 2560 67 / 58.5; 2048 x 4096 x 4096 29.7 / 22.4).
+  const int64_t tiles = per * a.world, rem = large ? tiles % cus : 0;
+  const int64_t halves = 2 * rem <= cus ? rem : 0;
+  a.n_full = static_cast<int>(tiles - halves);
+  const unsigned blocks = static_cast<unsigned>(tiles + halves);
   const hipError_t e = large ? launch_tiles<MxL, O>(a, blocks, s) : launch_tiles<MxS, O>(a, blocks, s);
   return e == hipSuccess ? MC2_OK : MC2_ERR_HIP;
 }

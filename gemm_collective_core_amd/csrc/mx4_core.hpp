@@ -92,7 +92,9 @@ struct MxTile {
   static constexpr int FM = WTM / 32, FN = WTN / 32;
   static constexpr int NT = 256;
   static constexpr int kABytes = BM * kKBytes, kBBytes = BN * kKBytes;
-  static constexpr int kScBytes = (BM + BN) * 16;  // one pair of stages
+  // scales of a pair of stages: loads of 64 rows, the same number for every wave
+  static constexpr int NS = (BM + BN + 255) / 256;
+  static constexpr int kScBytes = 4 * NS * 1024;
   static constexpr int kSc0 = 2 * (kABytes + kBBytes);
   static constexpr int kLoopBytes = kSc0 + 2 * kScBytes;
 };
@@ -114,9 +116,9 @@ __device__ __forceinline__ void mainloop_mx4(lds_t* smem, const MxSide& a, const
                                              f32x16_t (&acc)[TS::FM][TS::FN]) {
   constexpr int FM = TS::FM, FN = TS::FN, MM = FM * FN, Q = 4 * MM;
   constexpr int NA = TS::BM / 32, NB = TS::BN / 32, NL = NA + NB;  // loads a wave, 8 rows each
-  constexpr int NS = (TS::BM + TS::BN) / 256;  // scale loads a wave, 64 rows each, per two stages
+  constexpr int NS = TS::NS;  // scale loads a wave, 64 rows each, per two stages
   constexpr int NF = FM + FN;                  // operand reads per k-step
-  static_assert(NS * 256 == TS::BM + TS::BN, "a scale load for every wave");
+  static_assert(TS::BM % 64 == 0 && TS::BN % 64 == 0, "a scale load is of one side");
   // slots of a stage, one MFMA each: the reads of k-steps 1 to 3 (RS a slot),
   // kBarA (wait for them; the buffer is free), the loads of the stage after
   // next spread over the rest, kBarB (this wave's loads of the next stage have
@@ -159,7 +161,8 @@ __device__ __forceinline__ void mainloop_mx4(lds_t* smem, const MxSide& a, const
     const bool isa = 64 * (NS * wave + j) < TS::BM;
     const int rr = isa ? r : r - TS::BM;
     const int64_t last = isa ? a.last : b.last;
-    s_off[j] = static_cast<uint32_t>((rr < last ? rr : last) * pitch);
+    // (past the last row of both sides: nothing is loaded)
+    s_off[j] = r < TS::BM + TS::BN ? static_cast<uint32_t>((rr < last ? rr : last) * pitch) : kOffNone;
   }
 
   const int n = static_cast<int>((nb + 7) / 8);
