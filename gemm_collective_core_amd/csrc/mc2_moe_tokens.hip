@@ -100,8 +100,15 @@ __device__ __forceinline__ Expert pick_expert(const TokArgs& p, int a, PickMem& 
   }
   if (threadIdx.x == 0) mem.count = 0;
   __syncthreads();
-  for (int s = threadIdx.x; s < p.TK; s += NT)
-    if (p.sel[s] - p.e0 == a) mem.list[atomicAdd(&mem.count, 1)] = static_cast<uint16_t>(s);
+  for (int b = threadIdx.x; b < p.TK; b += 4 * NT) {  // four loads in flight
+    int id[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = p.sel[b + i * NT < p.TK ? b + i * NT : p.TK - 1] - p.e0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (id[i] == a && b + i * NT < p.TK)
+        mem.list[atomicAdd(&mem.count, 1)] = static_cast<uint16_t>(b + i * NT);
+  }
   __syncthreads();
   r.count = __builtin_amdgcn_readfirstlane(mem.count);
   if (r.count > 0) r.e = a;
@@ -175,11 +182,26 @@ __device__ __forceinline__ void count_slots(const TokArgs& p, int t) {
 // in groups of U neighbouring steps a wave: Group holds this lane's part of one.
 // load(st, step, u) brings step u of a group into registers and scales(st, step)
 // what its U steps share, which take() puts in force; frag<T>(u, f) is the
-// operand of fragment f (16 columns) for sub-step T of KT, 32 K values each.
-// k0(s, T, g): first of the eight K values that lane group g holds of it.
+// operand of fragment f (16 columns) for sub-step T of KT, 32 K values each. The
+// rows' operands are loaded with row_k(s, T, g) the first of the eight K values
+// that lane group g loads, and order(a) then gives every lane the values that
+// frag<T> goes with.
 // Column c of the strip is lane lane_of(c) & 15 of fragment frag_of(c).
 // (Addresses are 32-bit offsets from scalar bases: 64-bit ones would take two
 // registers for each load in flight.)
+
+// Exchange the upper 32 lanes of a with the lower 32 of b; the odd rows of 16
+// lanes of a with the even ones of b.
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
 
 // bf16 weights (rows of K, columns contiguous): a lane loads LC neighbouring
 // columns of eight K rows; the eight values of a column then lie in one lane
@@ -236,7 +258,8 @@ struct WBf16 {
       return bit_cast<bf16x8_t>(v);
     }
   };
-  static __device__ __forceinline__ int64_t k0(int64_t s, int, int g) { return s * 32 + 8 * g; }
+  static __device__ __forceinline__ int64_t row_k(int64_t s, int, int g) { return s * 32 + 8 * g; }
+  static __device__ __forceinline__ void order(u32x4_t (&)[1]) {}
   static __device__ __forceinline__ int frag_of(int c) { return c % LC; }
   static __device__ __forceinline__ int lane_of(int c) { return c / LC; }
 };
@@ -318,8 +341,23 @@ struct WMx4 {
       return bit_cast<bf16x8_t>(mx4_bf16x8(c[u][f][T], mx4_scale(byte)));
     }
   };
-  static __device__ __forceinline__ int64_t k0(int64_t s, int t, int g) {
-    return s * 128 + 32 * g + 8 * t;
+  // Sub-step T goes with K values 32 g + 8 T + .. of lane group g. A load of those
+  // would touch 16 bytes in every 64 of a row; instead the four groups load 64
+  // contiguous bytes, 32 T + 8 g + .., and the 4 x 4 pieces (T, g) change places.
+  static __device__ __forceinline__ int64_t row_k(int64_t s, int t, int g) {
+    return s * 128 + 32 * t + 8 * g;
+  }
+  static __device__ __forceinline__ void order(u32x4_t (&a)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t r[4] = {a[0][i], a[1][i], a[2][i], a[3][i]};
+      swap32(r[0], r[2]);
+      swap32(r[1], r[3]);
+      swap16(r[0], r[1]);
+      swap16(r[2], r[3]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) a[t][i] = r[t];
+    }
   }
   static __device__ __forceinline__ int frag_of(int c) { return c / 16; }
   static __device__ __forceinline__ int lane_of(int c) { return c % 16; }
@@ -383,16 +421,16 @@ __device__ __forceinline__ void fc1_rows(const TokArgs& p, int64_t e, const uint
     const int r = 16 * i + (lane & 15);
     xr[i] = r < count ? static_cast<uint32_t>(list[r] / p.K * p.H * 2) : kOffNone;
   }
-  u32x4_t a[U][W::KT][MT];
+  u32x4_t a[U][MT][W::KT];
   auto load_rows = [&](int grp) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < W::KT; ++t) {
-        const int64_t k = W::k0(step(grp, u), t, g);
+        const int64_t k = W::row_k(step(grp, u), t, g);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-          a[u][t][i] = __builtin_amdgcn_raw_buffer_load_b128(
+          a[u][i][t] = __builtin_amdgcn_raw_buffer_load_b128(
               rx, k < p.H ? xr[i] + static_cast<uint32_t>(2 * k) : kOffNone, 0, 0);
       }
   };
@@ -408,6 +446,12 @@ __device__ __forceinline__ void fc1_rows(const TokArgs& p, int64_t e, const uint
       const int ng = turn ? 0 : grp + 1;
       const bool more = !turn || s + 1 < s1;
       if (turn && more) at_strip(s + 1);
+      if (s == s0 || groups > 1) {  // rows newly loaded
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) W::order(a[u][i]);
+      }
       wg.take();
       wu.take();
       if (more) {
@@ -423,8 +467,8 @@ __device__ __forceinline__ void fc1_rows(const TokArgs& p, int64_t e, const uint
             const bf16x8_t bg = wg.template frag<t>(u, f), bu = wu.template frag<t>(u, f);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-              ag[f][i] = mfma_bf16(bit_cast<bf16x8_t>(a[u][t][i]), bg, ag[f][i]);
-              au[f][i] = mfma_bf16(bit_cast<bf16x8_t>(a[u][t][i]), bu, au[f][i]);
+              ag[f][i] = mfma_bf16(bit_cast<bf16x8_t>(a[u][i][t]), bg, ag[f][i]);
+              au[f][i] = mfma_bf16(bit_cast<bf16x8_t>(a[u][i][t]), bu, au[f][i]);
             }
           }
         });
@@ -530,18 +574,18 @@ __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint
     const int r = 16 * i + (lane & 15);
     hr[i] = r < count ? static_cast<uint32_t>(list[r] * p.I * 2) : kOffNone;
   }
-  u32x4_t hi[U][W::KT][MT], lo[U][W::KT][MT];
+  u32x4_t hi[U][MT][W::KT], lo[U][MT][W::KT];
   auto load_rows = [&](int grp) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < W::KT; ++t) {
-        const int64_t k = W::k0(step(grp, u), t, g);
+        const int64_t k = W::row_k(step(grp, u), t, g);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           const uint32_t off = k < p.I ? hr[i] + static_cast<uint32_t>(2 * k) : kOffNone;
-          hi[u][t][i] = __builtin_amdgcn_raw_buffer_load_b128(rhi, off, 0, 0);
-          lo[u][t][i] = __builtin_amdgcn_raw_buffer_load_b128(rlo, off, 0, 0);
+          hi[u][i][t] = __builtin_amdgcn_raw_buffer_load_b128(rhi, off, 0, 0);
+          lo[u][i][t] = __builtin_amdgcn_raw_buffer_load_b128(rlo, off, 0, 0);
         }
       }
   };
@@ -557,6 +601,15 @@ __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint
       const int ng = turn ? 0 : grp + 1;
       const bool more = !turn || s + 1 < s1;
       if (turn && more) at_strip(s + 1);
+      if (s == s0 || groups > 1) {  // rows newly loaded
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            W::order(hi[u][i]);
+            W::order(lo[u][i]);
+          }
+      }
       w.take();
       if (more) w.scales(sw, step(ng, 0));
 #pragma unroll
@@ -568,8 +621,8 @@ __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint
             const bf16x8_t b = w.template frag<t>(u, f);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-              acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(hi[u][t][i]), b, acc[f][i]);
-              acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(lo[u][t][i]), b, acc[f][i]);
+              acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(hi[u][i][t]), b, acc[f][i]);
+              acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(lo[u][i][t]), b, acc[f][i]);
             }
           }
         });
