@@ -232,3 +232,24 @@ def test_agrees_with_the_path_for_many_tokens():
     err = (out.double() - many.double()).abs()
     assert (err <= 2.0 ** -7 * out.double().abs() + 2.0 ** -6 * rms).all()
     assert err.square().mean().sqrt() <= 2.0 ** -8 * 1.5 * rms
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("T", [1, 24])
+def test_weights_beyond_2_31_elements(T, mx4):
+    """64 equal experts, 2.4e9 elements of w1: the last gives the first's output."""
+    H, I, E, K = 4096, 4608, 64, 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w1 = (0.02 * torch.randn((1, H, 2 * I), generator=g, device="cuda")).to(BF)
+    w2 = (0.02 * torch.randn((1, I, H), generator=g, device="cuda")).to(BF)
+    x = torch.randn((T, H), generator=g, device="cuda").to(BF)
+    probs = torch.rand((T, K), generator=g, device="cuda")
+    kw = dict(num_experts=E, ep_rank=0)
+    if mx4:
+        (w1, s1), (w2, s2) = (mc2.mc2_mx4_quantize(w, trans=True) for w in (w1, w2))
+        kw.update(w1_scale=s1.repeat(E, 1, 1), w2_scale=s2.repeat(E, 1, 1))
+    w1, w2 = w1.repeat(E, 1, 1), w2.repeat(E, 1, 1)
+    outs = [mc2.mc2_moe_tokens(x, torch.full((T, K), e, dtype=torch.int32, device="cuda"), probs,
+                               w1, w2, **kw) for e in (0, 31, E - 1)]
+    assert outs[0].abs().max() > 0.01
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
