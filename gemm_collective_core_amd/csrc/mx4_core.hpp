@@ -7,8 +7,9 @@
 // of the 16-bit loops. What differs:
 //  * v_mfma_scale_f32_32x32x64_f8f6f4, four k-steps a stage. Lane l supplies 32
 //    values (16 bytes) of row l & 31; in k-step j the lanes of group g = l >> 5
-//    take the stage's block 4 g + j. (The 16 x 16 x 128 shape reaches 60% of
-//    its rate in registers: 4.4 against 7.3 PFLOP/s on this card.)
+//    take the stage's block 4 g + j. (The loop in the 16 x 16 x 128 shape, with
+//    the 16-bit loop's order of a stage, takes the same time at long K, 484 us
+//    at 16384 x 8192 x 8192, and 127.5 against 119 us at k = 1024.)
 //  * The powers of two go to the instruction as one byte a lane, picked from a
 //    register by the instruction itself: the four blocks that a lane takes in a
 //    stage are neighbours, so one 4-byte LDS read per 32 rows and stage brings
@@ -19,6 +20,9 @@
 //    slots (the accumulators live in the accumulation registers, which leaves
 //    128 vector registers for a stage's operands), which frees the buffer for
 //    the loads of the stage after next for the rest of the stage.
+// Bound by the matrix pipes at the clock that their power leaves: 16384 x 8192 x
+// 3584 takes 225 us (4.3 PFLOP/s, 1.8 GHz, pipes busy 60% of a tile's time);
+// without any loads the same loop takes 207.
 #pragma once
 
 #include <utility>
