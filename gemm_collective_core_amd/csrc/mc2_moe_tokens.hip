@@ -33,7 +33,7 @@ namespace mc2 {
 constexpr int kTokMaxSlots = 4096;   // T * K
 constexpr int kTokMaxExperts = 1024;
 constexpr int kCpolAgent = 0x10;     // sc1: coherent over the XCDs' L2s
-constexpr int kTokMaxPer = 64;       // strips a workgroup
+constexpr int kTokMaxPer = 2;        // strips a workgroup
 constexpr int kTokMany = 2;          // 16-row operands at a time where an expert has more slots
                                      // (four would leave one workgroup a CU its registers)
 
@@ -217,6 +217,7 @@ template <int LC_>
 struct WBf16 {
   static constexpr int NF = LC_, LC = LC_, KS = 32, KT = 1, NW = 8;
   static constexpr int U1 = LC_ == 2 ? 4 : 2, U2 = 4;  // steps a group, fc1 and fc2
+  static constexpr int U1m = U1, U2m = U2;             // ... of kTokMany operands
 
   struct Strip {
     const char* base;  // column 0 of the strip in K row 0
@@ -278,7 +279,7 @@ struct WBf16 {
 template <int NF_>
 struct WMx4 {
   static constexpr int NF = NF_, KS = 128, KT = 4, NW = 4;
-  static constexpr int U1 = 4, U2 = 2;
+  static constexpr int U1 = 4, U2 = 2, U1m = 2, U2m = 1;
 
   struct Strip {
     const char* base;
@@ -401,7 +402,7 @@ template <class W, int MT>
 __device__ __forceinline__ void fc1_rows(const TokArgs& p, int64_t e, const uint16_t* list,
                                          int count, int s0, int s1,
                                          f32x4_t (&red)[W::NW][2 * W::NF][64]) {
-  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U1 : W::U1 / 2, CW = 16 * NF;
+  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U1 : W::U1m, CW = 16 * NF;
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int groups = static_cast<int>((p.H + W::KS * NW * U - 1) / (W::KS * NW * U));
@@ -557,7 +558,7 @@ template <class W, int MT>
 __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint16_t* list,
                                          int count, int s0, int s1,
                                          f32x4_t (&red)[W::NW][W::NF][64]) {
-  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U2 : W::U2 / 2, CW = 16 * NF;
+  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U2 : W::U2m, CW = 16 * NF;
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int groups = static_cast<int>((p.I + W::KS * NW * U - 1) / (W::KS * NW * U));
@@ -760,11 +761,13 @@ static bool tok_workspace(int64_t T, int K, int64_t H, int64_t I, TokWorkspace& 
   return true;
 }
 
-// Strips a workgroup, so that about six workgroups a CU remain (64 tokens above, 1
-// / 2 / 3 / 4 strips a workgroup in both kernels: 115 / 108 / 116 / 137 us).
+// Strips a workgroup: two where twelve workgroups a CU would each have one (us at
+// 1 / 2 / 3 / as many as leave six workgroups a CU: 64 tokens above, MX4, 115 / 108
+// / 116 / 108; 256 tokens of 1024 / 256, 8 of 1024 experts, MX4 209 / 165 / 168 /
+// 271, of 512 experts, bf16 254 / 223 / 228 / 239): the second strip's weights are
+// on their way while the first one's sums are made.
 static int strips_per(int64_t strips, int64_t rows, int64_t cus) {
-  const int64_t per = strips * rows / (6 * cus);
-  return static_cast<int>(per < 1 ? 1 : per < kTokMaxPer ? per : kTokMaxPer);
+  return strips * rows >= 12 * cus ? kTokMaxPer : 1;
 }
 
 template <class W1, class W2, bool MANY>
