@@ -395,23 +395,29 @@ __device__ __forceinline__ float tile_sum(const f32x4_t (&red)[NW][NV][64], int 
 // U K steps ahead: a step's registers are loaded again for the next group, of
 // this strip or the next, as soon as its products are done, so that memory is
 // read on while the waves' sums meet in LDS. Where one group covers K, the rows'
-// operands are loaded once for all strips.
+// operands are loaded once for all strips. A wave takes V neighbouring steps of K
+// in every V * NW, in this order whatever U is: the sums of a slot are then the
+// same bits however many slots share its operand (which varies, see pick_expert).
 
 // h of up to 16 * MT slots, list[0 .. count).
 template <class W, int MT>
 __device__ __forceinline__ void fc1_rows(const TokArgs& p, int64_t e, const uint16_t* list,
                                          int count, int s0, int s1,
                                          f32x4_t (&red)[W::NW][2 * W::NF][64]) {
-  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U1 : W::U1m, CW = 16 * NF;
+  constexpr int NF = W::NF, NW = W::NW, V = W::U1, U = MT == 1 ? V : W::U1m, CW = 16 * NF;
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int groups = static_cast<int>((p.H + W::KS * NW * U - 1) / (W::KS * NW * U));
+  const int groups = static_cast<int>((p.H + W::KS * NW * V - 1) / (W::KS * NW * V)) * (V / U);
   typename W::Strip sg, su;
   auto at_strip = [&](int s) {
     sg = W::strip(p.w1, p.w1s, e, p.H, 2 * p.I, 0, static_cast<int64_t>(s) * CW, p.I);
     su = W::strip(p.w1, p.w1s, e, p.H, 2 * p.I, p.I, static_cast<int64_t>(s) * CW, p.I);
   };
-  auto step = [&](int grp, int u) { return static_cast<int64_t>((grp * NW + wave) * U + u); };
+  static_assert(V % U == 0, "groups are parts of V steps");
+  auto step = [&](int grp, int u) {
+    const int q = grp * U + u;
+    return static_cast<int64_t>((q / V * NW + wave) * V + q % V);
+  };
   typename W::template Group<U> wg, wu;
   at_strip(s0);
   wg.scales(sg, step(0, 0));
@@ -558,15 +564,19 @@ template <class W, int MT>
 __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint16_t* list,
                                          int count, int s0, int s1,
                                          f32x4_t (&red)[W::NW][W::NF][64]) {
-  constexpr int NF = W::NF, NW = W::NW, U = MT == 1 ? W::U2 : W::U2m, CW = 16 * NF;
+  constexpr int NF = W::NF, NW = W::NW, V = W::U2, U = MT == 1 ? V : W::U2m, CW = 16 * NF;
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int groups = static_cast<int>((p.I + W::KS * NW * U - 1) / (W::KS * NW * U));
+  const int groups = static_cast<int>((p.I + W::KS * NW * V - 1) / (W::KS * NW * V)) * (V / U);
   typename W::Strip sw;
   auto at_strip = [&](int s) {
     sw = W::strip(p.w2, p.w2s, e, p.I, p.H, 0, static_cast<int64_t>(s) * CW, p.H);
   };
-  auto step = [&](int grp, int u) { return static_cast<int64_t>((grp * NW + wave) * U + u); };
+  static_assert(V % U == 0, "groups are parts of V steps");
+  auto step = [&](int grp, int u) {
+    const int q = grp * U + u;
+    return static_cast<int64_t>((q / V * NW + wave) * V + q % V);
+  };
   typename W::template Group<U> w;
   at_strip(s0);
   w.scales(sw, step(0, 0));

@@ -253,3 +253,22 @@ def test_weights_beyond_2_31_elements(T, mx4):
                                w1, w2, **kw) for e in (0, 31, E - 1)]
     assert outs[0].abs().max() > 0.01
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("T", [40, 48, 61, 256])
+def test_a_token_does_not_depend_on_its_place(T, mx4):
+    """Many slots of one expert are taken in groups of different sizes, in no
+    particular order: a token's bits are the same in every group, so that they are
+    the same in every call."""
+    H, I, E, K = 1032, 776, 4, 2
+    x, _, probs, w1, w2 = (t.cuda() for t in drawn(T, H, I, E, E, K, 17))
+    sel = torch.tensor([1, 3], dtype=torch.int32, device="cuda").expand(T, 2).contiguous()
+    kw = dict(ep_rank=0, num_experts=E)
+    if mx4:
+        (w1, s1), (w2, s2) = (mc2.mc2_mx4_quantize(w, trans=True) for w in (w1, w2))
+        kw.update(w1_scale=s1, w2_scale=s2)
+    out = mc2.mc2_moe_tokens(x, sel, probs, w1, w2, **kw)
+    for shift in (1, T // 2, T - 5):
+        got = mc2.mc2_moe_tokens(x.roll(shift, 0), sel, probs.roll(shift, 0), w1, w2, **kw)
+        assert torch.equal(got, out.roll(shift, 0)), shift
