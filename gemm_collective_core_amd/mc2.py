@@ -683,15 +683,17 @@ def mc2_mx4_quantize(x, *, trans=False, codes=None, scales=None):
     if x.dim() not in (2, 3):
         raise ValueError("x must be a matrix or a stack of matrices")
     _want(x, "x", dtypes=_MX4_TYPES)
-    k, rows = (x.shape[-2], x.shape[-1]) if trans else (x.shape[-1], x.shape[-2])
-    lead = x.shape[:-2]
-    _want_mx4(codes, scales, "codes", (*lead, rows), k, given=False)
+    *lead, rows, k = x.shape
+    if trans:
+        rows, k = k, rows
+    if codes is not None or scales is not None:
+        _want_mx4(codes, scales, "codes", (*lead, rows), k, given=False)
     dev = _dev(x, codes, scales)
     if codes is None:
         codes = torch.empty((*lead, rows, _mx4_row(k)), dtype=torch.uint8, device=dev)
     if scales is None:
         scales = torch.empty((*lead, rows, _mx4_pitch(k)), dtype=torch.uint8, device=dev)
-    batch = 1 if x.dim() == 2 else x.shape[0]
+    batch = lead[0] if lead else 1
     st = _call(dev, _lib.load().mc2_mx4_quantize, x.data_ptr(), batch, rows, k, int(bool(trans)),
                _CODES[x.dtype], codes.data_ptr(), scales.data_ptr(), _stream(dev))
     _check("mc2_mx4_quantize", st)
@@ -703,17 +705,18 @@ def mc2_mx4_dequantize(codes, scales, k, *, trans=False, out_dtype=torch.bfloat1
     scales stand for, in out_dtype (bf16, fp16 or fp32)."""
     if codes.dim() not in (2, 3):
         raise ValueError("codes must be (rows, bytes) or a stack of them")
-    lead, rows = codes.shape[:-2], codes.shape[-2]
+    *lead, rows, _ = codes.shape
     _want_mx4(codes, scales, "codes", (*lead, rows), k)
     shape = (*lead, k, rows) if trans else (*lead, rows, k)
     out_dtype = out_dtype if out is None else out.dtype
     if out_dtype not in _MX4_TYPES:
         raise ValueError(f"out_dtype must be one of {_MX4_TYPES}, got {out_dtype}")
-    _want(out, "out", shape=shape)
+    if out is not None:
+        _want(out, "out", shape=shape)
     dev = _dev(codes, scales, out)
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=dev)
-    batch = 1 if codes.dim() == 2 else codes.shape[0]
+    batch = lead[0] if lead else 1
     st = _call(dev, _lib.load().mc2_mx4_dequantize, codes.data_ptr(), scales.data_ptr(), batch,
                rows, k, int(bool(trans)), _CODES[out_dtype], out.data_ptr(), _stream(dev))
     _check("mc2_mx4_dequantize", st)
@@ -806,7 +809,8 @@ def mc2_moe_tokens(x, sel, probs, w1, w2, *, ep_rank, num_experts, w1_scale=None
     dev = _dev(x, sel, probs, w1, w2, w1_scale, w2_scale, out, workspace, dev_err)
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    workspace = _workspace(mc2_moe_tokens_workspace_size(T, K, H, I), workspace, dev)
+    if workspace is None:
+        workspace = _workspace(mc2_moe_tokens_workspace_size(T, K, H, I), None, dev)
     st = _call(dev, _lib.load().mc2_moe_tokens, x.data_ptr(), sel.data_ptr(), probs.data_ptr(), T,
                K, H, num_experts, ep_rank, E_l, MC2_MX4 if mx4 else MC2_BF16, w1.data_ptr(),
                _ptr(w1_scale), w2.data_ptr(), _ptr(w2_scale), I, out.data_ptr(),
