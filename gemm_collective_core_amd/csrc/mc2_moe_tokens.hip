@@ -563,7 +563,8 @@ __global__ __launch_bounds__(W::NW * 64, 2) void tokens_fc1_kernel(TokArgs p) {
 template <class W, int MT>
 __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint16_t* list,
                                          int count, int s0, int s1,
-                                         f32x4_t (&red)[W::NW][W::NF][64]) {
+                                         f32x4_t (&red)[W::NW][W::NF][64],
+                                         uint16_t (&slots)[16 * kTokMany]) {
   constexpr int NF = W::NF, NW = W::NW, V = W::U2, U = MT == 1 ? V : W::U2m, CW = 16 * NF;
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -607,6 +608,9 @@ __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint
       }
   };
   load_rows(0);
+  // the slots again, in LDS: a load of them after the products would wait for
+  // every load that is under way by then (there before the sums' barrier)
+  if (threadIdx.x < count) slots[threadIdx.x] = list[threadIdx.x];
   for (int s = s0; s < s1; ++s) {
     f32x4_t acc[NF][MT];
 #pragma unroll
@@ -658,7 +662,7 @@ __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint
         const int m = q / CW, c = q - m * CW;
         if (c0 + c >= p.H) continue;
         const float v = tile_sum<NW>(red, W::frag_of(c), m, W::lane_of(c));
-        const int64_t at = static_cast<int64_t>(list[16 * i + m]) * p.H + c0 + c;
+        const int64_t at = static_cast<int64_t>(slots[16 * i + m]) * p.H + c0 + c;
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ry, static_cast<int>(at * 4), 0,
                                               kCpolAgent);
       }
@@ -679,11 +683,12 @@ __device__ __forceinline__ void sum_slots(const TokArgs& p, int t, int64_t c) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int s = t * p.K + (k0 + j < p.K ? k0 + j : p.K - 1);
+      // (rows of slots that are not local are read too, and dropped: the loads do
+      // not wait for the ids)
       in[j] = k0 + j < p.K && local_id(p, s) >= 0;
       w[j] = p.probs[s];
       y[j] = __builtin_amdgcn_raw_buffer_load_b128(
-          ry, in[j] ? static_cast<uint32_t>((static_cast<int64_t>(s) * p.H + c) * 4) : kOffNone, 0,
-          kCpolAgent);
+          ry, static_cast<uint32_t>((static_cast<int64_t>(s) * p.H + c) * 4), 0, kCpolAgent);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -701,6 +706,7 @@ template <class W, bool MANY>
 __global__ __launch_bounds__(W::NW * 64, 2) void tokens_fc2_kernel(TokArgs p) {
   constexpr int NT = W::NW * 64, CW = 16 * W::NF;
   __shared__ f32x4_t red[W::NW][W::NF][64];
+  __shared__ uint16_t slots[16 * kTokMany];
   __shared__ uint16_t done[kTokDone];  // strip (from the workgroup's first) * 256 + token
   __shared__ int ndone;
   const i32x4_t plan = p.plan[blockIdx.y];
@@ -712,10 +718,10 @@ __global__ __launch_bounds__(W::NW * 64, 2) void tokens_fc2_kernel(TokArgs p) {
     const int left = count - b;
     if (MANY && left > 16) {
       fc2_rows<W, kTokMany>(p, plan[0], list + b, left < 16 * kTokMany ? left : 16 * kTokMany,
-                            st.s0, st.s1, red);
+                            st.s0, st.s1, red, slots);
       b += 16 * kTokMany;
     } else {
-      fc2_rows<W, 1>(p, plan[0], list + b, left < 16 ? left : 16, st.s0, st.s1, red);
+      fc2_rows<W, 1>(p, plan[0], list + b, left < 16 ? left : 16, st.s0, st.s1, red, slots);
       b += 16;
     }
   }
