@@ -21,10 +21,10 @@
 // which load nothing, and are dropped: rows of a product do not mix, so neither
 // do their NaN.
 //
-// Measured, fc1 and fc2: one token of the layer above 14.5 + 10.1 us (75 MB, 3.1
-// TB/s); 64 tokens, all 128 experts in MX4, 53 + 50 us (316 MB). Bound by chains
+// Measured, fc1 and fc2: one token of the layer above 14.8 + 9.6 us (75 MB, 3.1
+// TB/s); 64 tokens, all 128 experts in MX4, 52 + 46 us (316 MB). Bound by chains
 // of latencies (ids, rows, products, LDS, y, counter, sum) with two workgroups a
-// CU: without any read of w1 the 64 tokens still take 87 of 109 us.
+// CU: without any read of w1 the 64 tokens still took 87 of 109 us.
 #include "mc2_mx4.hpp"
 #include "mc2_tiles.hpp"
 
