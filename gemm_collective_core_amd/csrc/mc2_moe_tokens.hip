@@ -8,7 +8,7 @@
 //   tokens_fc1_kernel: a workgroup computes a strip of gate columns and the same
 //     strip of up columns for all the rows of one expert, each wave over a part
 //     of H; the waves' sums meet in LDS, SwiGLU follows, and h leaves as the sum
-//     of two bf16 numbers.
+//     of three bf16 numbers, all the 24 bits of fp32 (see split_h).
 //   tokens_fc2_kernel: the same with h and w2 for a strip of output columns. The
 //     results y of a slot stay fp32 in the workspace; the workgroup that brings
 //     the last one of a token adds the token's strip up, in slot order, with the
@@ -34,6 +34,7 @@ constexpr int kTokMaxSlots = 4096;   // T * K
 constexpr int kTokMaxExperts = 1024;
 constexpr int kCpolAgent = 0x10;     // sc1: coherent over the XCDs' L2s
 constexpr int kTokMaxPer = 2;        // strips a workgroup
+constexpr int kHParts = 3;           // bf16 numbers that hold an h
 constexpr int kTokMany = 2;          // 16-row operands at a time where an expert has more slots
                                      // (four would leave one workgroup a CU its registers)
 
@@ -52,8 +53,7 @@ struct TokArgs {
   int32_t* left;      // (strip of fc2, token): local slots whose y is still to come
   i32x4_t* plan;      // expert, slots, place of the first in list, experts named
   uint16_t* list;     // local slots, expert after expert
-  uint16_t* h_hi;
-  uint16_t* h_lo;
+  uint16_t* h[kHParts];
   float* y;
   int32_t* dev_err;
   int64_t H, I;
@@ -189,9 +189,10 @@ __device__ __forceinline__ void count_slots(const TokArgs& p, int t) {
 // load(st, step, u) brings step u of a group into registers and scales(st, step)
 // what its U steps share, which take() puts in force; frag<T>(u, f) is the
 // operand of fragment f (16 columns) for sub-step T of KT, 32 K values each. The
-// rows' operands are loaded with row_k(s, T, g) the first of the eight K values
-// that lane group g loads, and order(a) then gives every lane the values that
-// frag<T> goes with.
+// rows of x are loaded with row_k(s, T, g) the first of the eight K values that
+// lane group g loads, and order(a) then gives every lane the values that frag<T>
+// goes with. h is written in the lanes' order instead: frag<T> goes with the eight
+// values from lane_k(s, T, g) on, and value k of a row of K stands at h_at(k, K).
 // Column c of the strip is lane lane_of(c) & 15 of fragment frag_of(c).
 // (Addresses are 32-bit offsets from scalar bases: 64-bit ones would take two
 // registers for each load in flight.)
@@ -267,6 +268,8 @@ struct WBf16 {
   };
   static __device__ __forceinline__ int64_t row_k(int64_t s, int, int g) { return s * 32 + 8 * g; }
   static __device__ __forceinline__ void order(u32x4_t (&)[1]) {}
+  static __device__ __forceinline__ int64_t lane_k(int64_t s, int, int g) { return s * 32 + 8 * g; }
+  static __device__ __forceinline__ int64_t h_at(int64_t k, int64_t) { return k; }
   static __device__ __forceinline__ int frag_of(int c) { return c % LC; }
   static __device__ __forceinline__ int lane_of(int c) { return c / LC; }
 };
@@ -366,6 +369,18 @@ struct WMx4 {
       for (int t = 0; t < 4; ++t) a[t][i] = r[t];
     }
   }
+  static __device__ __forceinline__ int64_t lane_k(int64_t s, int t, int g) {
+    return s * 128 + 32 * g + 8 * t;
+  }
+  // Piece (T, g) of 128 values, T first; the last values of a row, K % 128 of them,
+  // are `full` groups of four pieces and `more` pieces of one further group.
+  static __device__ __forceinline__ int64_t h_at(int64_t k, int64_t K) {
+    const int64_t first = k & ~int64_t{127};
+    const int left = static_cast<int>(K - first < 128 ? K - first : 128) >> 3;
+    const int full = left >> 2, more = left & 3;
+    const int r = static_cast<int>(k - first), t = (r >> 3) & 3, g = r >> 5;
+    return first + 8 * (t * full + (t < more ? t : more) + g) + (r & 7);
+  }
   static __device__ __forceinline__ int frag_of(int c) { return c / 16; }
   static __device__ __forceinline__ int lane_of(int c) { return c % 16; }
 };
@@ -398,6 +413,22 @@ __device__ __forceinline__ float tile_sum(const f32x4_t (&red)[NW][NV][64], int 
 // operands are loaded once for all strips. A wave takes V neighbouring steps of K
 // in every V * NW, in this order whatever U is: the sums of a slot are then the
 // same bits however many slots share its operand (which varies, see pick_expert).
+
+// h as three bf16 numbers: the upper half of h, of what that leaves, and of what is
+// left then, eight bits each. They sum to h exactly (from 2^-110 on; below, the last
+// one leaves bf16's range), and none is larger, so that a finite h has finite parts.
+// (Two of them, 16 bits, took 10 us of 250 less at 256 tokens with 4-bit weights, 6
+// of 110 at 64; 25 in 10000 outputs were then not the nearest bf16 number to the
+// result in 64 bits, with three 2.)
+__device__ __forceinline__ void split_h(float h, uint32_t (&part)[kHParts]) {
+  // (an infinite h has no rest)
+  const bool finite = __builtin_fabsf(h) < __builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kHParts; ++i) {
+    part[i] = __float_as_uint(h) >> 16;
+    h = finite ? h - bf16_bits_to_f32(part[i]) : 0.f;
+  }
+}
 
 // h of up to 16 * MT slots, list[0 .. count).
 template <class W, int MT>
@@ -508,13 +539,11 @@ __device__ __forceinline__ void fc1_rows(const TokArgs& p, int64_t e, const uint
         if (c0 + c >= p.I) continue;
         const float gate = tile_sum<NW>(red, f, m, n), up = tile_sum<NW>(red, NF + f, m, n);
         const float h = gate / (1.f + __expf(-gate)) * up;
-        const uint16_t hi = f32_to_bf16_bits(h);
-        const float hf = bf16_bits_to_f32(hi);
-        // (an infinite h has no rest)
-        const float lo = __builtin_fabsf(hf) < __builtin_inff() ? h - hf : 0.f;
-        const int64_t at = static_cast<int64_t>(list[16 * i + m]) * p.I + c0 + c;
-        p.h_hi[at] = hi;
-        p.h_lo[at] = f32_to_bf16_bits(lo);
+        uint32_t part[kHParts];
+        split_h(h, part);
+        const int64_t at = static_cast<int64_t>(list[16 * i + m]) * p.I + W::h_at(c0 + c, p.I);
+#pragma unroll
+        for (int j = 0; j < kHParts; ++j) p.h[j][at] = static_cast<uint16_t>(part[j]);
       }
       lds_barrier();
     }
@@ -583,8 +612,6 @@ __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint
   w.scales(sw, step(0, 0));
 #pragma unroll
   for (int u = 0; u < U; ++u) w.load(sw, step(0, u), u);
-  const __amdgpu_buffer_rsrc_t rhi = make_rsrc(reinterpret_cast<const char*>(p.h_hi));
-  const __amdgpu_buffer_rsrc_t rlo = make_rsrc(reinterpret_cast<const char*>(p.h_lo));
   const __amdgpu_buffer_rsrc_t ry = make_rsrc(reinterpret_cast<const char*>(p.y));
   uint32_t hr[MT];
 #pragma unroll
@@ -592,19 +619,20 @@ __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint
     const int r = 16 * i + (lane & 15);
     hr[i] = r < count ? static_cast<uint32_t>(list[r] * p.I * 2) : kOffNone;
   }
-  u32x4_t hi[U][MT][W::KT], lo[U][MT][W::KT];
+  u32x4_t h[U][MT][W::KT][kHParts];
   auto load_rows = [&](int grp) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < W::KT; ++t) {
-        const int64_t k = W::row_k(step(grp, u), t, g);
+        const int64_t k = W::lane_k(step(grp, u), t, g);
+        const uint32_t at = static_cast<uint32_t>(2 * W::h_at(k, p.I));
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const uint32_t off = k < p.I ? hr[i] + static_cast<uint32_t>(2 * k) : kOffNone;
-          hi[u][i][t] = __builtin_amdgcn_raw_buffer_load_b128(rhi, off, 0, 0);
-          lo[u][i][t] = __builtin_amdgcn_raw_buffer_load_b128(rlo, off, 0, 0);
-        }
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < kHParts; ++j)
+            h[u][i][t][j] = __builtin_amdgcn_raw_buffer_load_b128(
+                make_rsrc(reinterpret_cast<const char*>(p.h[j])), k < p.I ? hr[i] + at : kOffNone, 0, 0);
       }
   };
   load_rows(0);
@@ -622,15 +650,6 @@ __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint
       const int ng = turn ? 0 : grp + 1;
       const bool more = !turn || s + 1 < s1;
       if (turn && more) at_strip(s + 1);
-      if (s == s0 || groups > 1) {  // rows newly loaded
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            W::order(hi[u][i]);
-            W::order(lo[u][i]);
-          }
-      }
       w.take();
       if (more) w.scales(sw, step(ng, 0));
 #pragma unroll
@@ -641,10 +660,10 @@ __device__ __forceinline__ void fc2_rows(const TokArgs& p, int64_t e, const uint
           for (int f = 0; f < NF; ++f) {
             const bf16x8_t b = w.template frag<t>(u, f);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(hi[u][i][t]), b, acc[f][i]);
-              acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(lo[u][i][t]), b, acc[f][i]);
-            }
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int j = 0; j < kHParts; ++j)
+                acc[f][i] = mfma_bf16(bit_cast<bf16x8_t>(h[u][i][t][j]), b, acc[f][i]);
           }
         });
         if (more) w.load(sw, step(ng, u), u);
@@ -772,7 +791,7 @@ static bool tok_workspace(int64_t T, int K, int64_t H, int64_t I, TokWorkspace& 
   w.plan = up256(static_cast<size_t>(tok_strips(H) * T) * 4);
   w.list = w.plan + up256(static_cast<size_t>(TK < kTokMaxExperts ? TK : kTokMaxExperts) * 16);
   w.h = w.list + up256(static_cast<size_t>(TK) * 2);
-  w.y = w.h + up256(static_cast<size_t>(TK * I) * 2) * 2;
+  w.y = w.h + up256(static_cast<size_t>(TK * I) * 2) * kHParts;
   w.bytes = w.y + up256(static_cast<size_t>(TK * H) * 4);
   return true;
 }
@@ -861,8 +880,8 @@ extern "C" int mc2_moe_tokens(const void* x, const int32_t* sel, const float* pr
   a.left = reinterpret_cast<int32_t*>(ws + w.left);
   a.plan = reinterpret_cast<i32x4_t*>(ws + w.plan);
   a.list = reinterpret_cast<uint16_t*>(ws + w.list);
-  a.h_hi = reinterpret_cast<uint16_t*>(ws + w.h);
-  a.h_lo = reinterpret_cast<uint16_t*>(ws + w.h + (w.y - w.h) / 2);
+  for (int j = 0; j < kHParts; ++j)
+    a.h[j] = reinterpret_cast<uint16_t*>(ws + w.h + (w.y - w.h) / kHParts * j);
   a.y = reinterpret_cast<float*>(ws + w.y);
   a.dev_err = dev_err;
   a.H = H;

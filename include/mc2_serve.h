@@ -114,8 +114,7 @@ int mc2_mx4_ag_mm_local(const void* x_gathered, const void* x_scale, const void*
  * E_l; a token with none gets a row of zeros, and the layer's output is the
  * sum of the ranks' outs. An id outside [0, num_experts) is skipped and sets
  * MC2_DEVERR_EXPERT_ID. An id may appear more than once in a token. Products
- * accumulate in fp32; h is held as the sum of two bf16 numbers (16 bits of
- * precision or more), y and the sum over k in fp32, one rounding to bf16.
+ * accumulate in fp32; h, y and the sum over k are fp32, one rounding to bf16.
  * Every expert named by a slot is read once (per 32 slots of it).
  *
  *   x, out (T, H) bf16; sel (T*K) int32; probs (T*K) fp32.

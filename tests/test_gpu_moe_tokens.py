@@ -272,3 +272,54 @@ def test_a_token_does_not_depend_on_its_place(T, mx4):
     for shift in (1, T // 2, T - 5):
         got = mc2.mc2_moe_tokens(x.roll(shift, 0), sel, probs.roll(shift, 0), w1, w2, **kw)
         assert torch.equal(got, out.roll(shift, 0)), shift
+
+
+def wide_h_case(T, I, K, seed):
+    """Every h has 24 significant bits, of which fc2's sums need the last. x is 128
+    at 0 (the gate, where silu is the identity in fp32) and 1 at three places of
+    blocks of their own, whose up weights 2^13, 2^3 and 2^-7 (or 2^-6, 2^-5) make
+    h = 2^20 + 2^10 + 1 (2, 4); its neighbour has h = 2^20 + 2^10, and w2 opposite
+    signs for the two. Sums are of whole numbers below I * 2^20.1 <= 2^24."""
+    g = torch.Generator().manual_seed(seed)
+    assert I <= 15
+    H, E = 128, 2
+    x = torch.zeros((T, H))
+    x[:, 0], x[:, 32], x[:, 64], x[:, 96] = 128, 1, 1, 1
+    w1 = torch.zeros((E, H, 2 * I))
+    w1[:, 0, :I] = 1
+    w1[:, 32, I:], w1[:, 64, I:] = 2.0 ** 13, 2.0 ** 3
+    w1[:, 96, I::2] = 2.0 ** -torch.randint(5, 8, (E, I // 2), generator=g).float()
+    w2 = torch.zeros((E, I, H))
+    w2[:, 0::2] = torch.randint(-1, 2, (E, I // 2, H), generator=g).float()
+    w2[:, 1::2] = -w2[:, 0::2]
+    sel = torch.randint(0, E, (T, K), generator=g, dtype=torch.int32)
+    return x.to(BF), sel, torch.ones((T, K)), w1.to(BF), w2.to(BF)
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("T,K", [(1, 1), (20, 1), (40, 2)])
+def test_h_keeps_all_the_bits_of_fp32(T, K, mx4):
+    case = wide_h_case(T, 8, K, T)
+    out = own(*case, mx4, ep_rank=0, num_experts=2)
+    ref, _, _ = ot.layer(*(f64(t) if t.dtype != torch.int32 else t.numpy() for t in case),
+                         ep_rank=0, num_experts=2)
+    assert np.abs(ref).max() >= 4
+    assert torch.equal(out.cpu(), torch.from_numpy(ref).to(BF))
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("T", [1, 20])
+def test_h_next_to_the_largest_number(T, mx4):
+    """h = 2^127 * 511/256, between the largest bf16 number (2^127 * 255/128) and
+    fp32's: finite, and so is the output, 2^117 * 511/256 rounded to even, 2^118."""
+    x, _, probs, w1, w2 = wide_h_case(T, 8, 1, 1)
+    w1[:, 32:, 8:] = 0
+    # up = 2^120 * 511/256 = 2^121 - 2^112
+    w1[:, 32, 8:], w1[:, 64, 8:] = 2.0 ** 121, -2.0 ** 112
+    w2[:] = 0
+    w2[:, 3, 5] = 2.0 ** -10
+    sel = torch.zeros((T, 1), dtype=torch.int32)
+    out = own(x, sel, probs, w1, w2, mx4, ep_rank=0, num_experts=2).cpu()
+    want = torch.zeros_like(out)
+    want[:, 5] = 2.0 ** 118
+    assert torch.equal(out, want)
