@@ -323,3 +323,38 @@ def test_h_next_to_the_largest_number(T, mx4):
     want = torch.zeros_like(out)
     want[:, 5] = 2.0 ** 118
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("T,H,I,K", [(3, 40, 72, 1), (20, 136, 136, 1), (40, 72, 264, 2)])
+def test_infinite_weights_of_named_experts(T, H, I, K, mx4):
+    """Where w2 holds infinities, y is what h @ w2 gives: infinite with the sign of
+    the products, NaN where signs differ or h is zero. In 4 bits an infinity is a
+    code whose value is past bf16's largest number: 2 held as 4 * 2^-1, its scale
+    raised to 2^126."""
+    E = 2
+    x, sel, probs, w1, w2 = integer_case(T, H, I, E, E, K, "top", 23)
+    w1[:, 0, :I] = 1  # silu is the identity
+    inf = float("inf")
+    w2[:, :, 5:9] = 0
+    for e in range(E):
+        w2[e, 1 + e, 5] = 2
+        w2[e, I - 1, 6] = -2
+        w2[e, 3, 7], w2[e, I - 2, 7] = 2, -2
+        w2[e, 2::3, 8] = 2
+    big = f64(w2)
+    big[:, :, 5:9] *= np.where(big[:, :, 5:9] == 0, 1, inf)
+    with np.errstate(invalid="ignore"):
+        ref, _, _ = ot.layer(f64(x), sel.numpy(), f64(probs), f64(w1), big, ep_rank=0, num_experts=E)
+    args = [t.cuda() for t in (x, sel, probs)]
+    if mx4:
+        (c1, s1), (c2, s2) = (mc2.mc2_mx4_quantize(w.cuda(), trans=True) for w in (w1, w2))
+        s2[:, 5:9, :(I + 31) // 32] = 253
+        out = mc2.mc2_moe_tokens(*args, c1, c2, w1_scale=s1, w2_scale=s2, ep_rank=0, num_experts=E)
+    else:
+        out = mc2.mc2_moe_tokens(*args, w1.cuda(), torch.from_numpy(big).to(BF).cuda(), ep_rank=0,
+                                 num_experts=E)
+    out, want = out.cpu(), torch.from_numpy(ref).to(BF)
+    assert want[:, 5:9].isinf().any() and not want[:, 5:9].isfinite().any()
+    assert torch.equal(out.isnan(), want.isnan())
+    assert torch.equal(out[~out.isnan()], want[~want.isnan()])
