@@ -358,3 +358,40 @@ def test_infinite_weights_of_named_experts(T, H, I, K, mx4):
     assert want[:, 5:9].isinf().any() and not want[:, 5:9].isfinite().any()
     assert torch.equal(out.isnan(), want.isnan())
     assert torch.equal(out[~out.isnan()], want[~want.isnan()])
+
+
+@pytest.mark.parametrize("mx4,T,H,I,E", [
+    # weights, tokens, sizes, experts: strips of fc1 a matrix, groups of K loads a strip
+    (True, 60, 72, 200, 512),     # 7 strips of 32 columns, the last of 8; one group
+    (True, 16, 72, 200, 512),
+    (True, 60, 2056, 200, 512),   # two groups, four for 17 slots or more
+    (True, 16, 2056, 232, 400),   # 8 strips
+    (False, 60, 72, 136, 1024),   # 3 strips of 64 columns, the last of 8; one group
+    (False, 16, 72, 136, 1024),
+    (False, 60, 1032, 136, 1024),  # three groups
+    (False, 16, 1032, 200, 800),  # 4 strips
+])
+def test_two_strips_a_workgroup(mx4, T, H, I, E):
+    """fc1 with so many workgroups that each takes two neighbouring strips, for
+    experts with 1, 11, 16, 17, 28 and 32 slots at a time. Only the experts named
+    hold numbers, the others NaN."""
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    strips = -(-I // (32 if mx4 else 64))
+    assert strips * E >= 12 * cus  # the rule of the launch
+    Ec, K = 24, 6
+    x, _, probs, w1, w2 = integer_case(T, H, I, Ec, Ec, K, "top", T + H)
+    g = torch.Generator().manual_seed(H)
+    sel = torch.randint(3, Ec, (T, K), generator=g, dtype=torch.int32)
+    sel[:, 0] = 0
+    sel[:, 4] = torch.where(torch.arange(T) < 17, 1, 2)
+    ref, mag, _ = ot.layer(f64(x), sel.numpy(), f64(probs), f64(w1), f64(w2), ep_rank=0,
+                           num_experts=Ec)
+    assert mag.max() < 2.0 ** 38 and np.abs(ref).max() < 2.0 ** 22
+    place = torch.cat([torch.tensor([0, E - 1]), 1 + torch.randperm(E - 2, generator=g)[:Ec - 2]])
+    big = []
+    for w in (w1, w2):
+        b = torch.full((E, *w.shape[1:]), float("nan"), dtype=BF, device="cuda")
+        b[place.cuda()] = w.cuda()
+        big.append(b)
+    out = own(x, place[sel.long()].to(torch.int32), probs, *big, mx4, ep_rank=0, num_experts=E)
+    assert torch.equal(out.cpu(), torch.from_numpy(ref).to(BF))
