@@ -216,3 +216,51 @@ def test_mm_chunks_and_flags(op, W, mc, turn):
             assert flags.cpu().tolist() == [epoch] * segs
             assert cnt.cpu().tolist() == [0] * segs
             assert torch.equal(out, want.to(t))
+
+
+def tiles_of(W, mc, turn, n):
+    """Tiles of a call with flags, which always takes the tiled kernel: (rows of a
+    tile, whole tiles, tiles that run as two halves)."""
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    sub = max(turn, 1)
+    pieces = [mc // sub + (j < mc % sub) for j in range(sub)] * W
+
+    def count(b):
+        return sum(-(-p // b) for p in pieces) * -(-n // b)
+    if 4 * count(256) <= cus:
+        return 128, count(128), 0
+    rem = count(256) % cus
+    return 256, count(256) - (rem if 2 * rem <= cus else 0), rem if 2 * rem <= cus else 0
+
+
+# W, rows a chunk, pieces, n, rows of a tile, whether tiles run whole, as halves
+TILED = [(1, 1000, 0, 1416, 128, True, False), (8, 1, 0, 24, 128, True, False),
+         (4, 130, 3, 264, 128, True, False), (2, 1150, 0, 2056, 256, False, True),
+         (1, 3000, 0, 2824, 256, True, False), (2, 1500, 5, 2824, 256, True, False),
+         (1, 4400, 0, 4096, 256, True, True), (2, 2200, 0, 4096, 256, True, True),
+         (4, 1100, 2, 4000, 256, True, True)]
+
+
+@pytest.mark.parametrize("W,mc,turn,n,bm,whole,halves", TILED)
+@pytest.mark.parametrize("k", [64, 256, 512, 520, 1000])
+def test_mm_tiles_exact_with_flags(W, mc, turn, n, bm, whole, halves, k):
+    """Every kind of tile, each with one stage of K, whole stages and a last part,
+    with and without a bias, in the three output types: the exact sums, every
+    segment's flag and counter. (Sums as in test_mm_exact.) Where whole and half
+    tiles meet, n_full lies inside a segment."""
+    assert tiles_of(W, mc, turn, n)[0] == bm
+    assert [v > 0 for v in tiles_of(W, mc, turn, n)[1:]] == [whole, halves]
+    m, segs = W * mc, W * max(turn, 1)
+    a, av = operand(m, k, k + 1)
+    b, bv = operand(n, k, k + 2)
+    bias = torch.randint(-64, 64, (n,), generator=torch.Generator().manual_seed(n)).bfloat16().cuda()
+    ref = torch.from_numpy(av).cuda() @ torch.from_numpy(bv).cuda().t().contiguous()
+    flags, cnt = (torch.zeros(segs, dtype=torch.int32, device="cuda") for _ in range(2))
+    f = mc2.mc2_mx4_mm_rs_local if k % 256 else mc2.mc2_mx4_ag_mm_local
+    for epoch, (t, bt) in enumerate(((torch.float32, None), (torch.float32, bias),
+                                     (torch.bfloat16, bias), (torch.float16, bias)), 1):
+        out = f(*a, *b, k, W, W - 1, bias=bt, out_dtype=t, ready_flags=flags, flag_counters=cnt,
+                epoch=epoch, comm_turn=turn)
+        want = ref if bt is None else ref + bt.double()
+        assert torch.equal(out, want.to(t)), t
+        assert flags.tolist() == [epoch] * segs and cnt.tolist() == [0] * segs
