@@ -264,3 +264,24 @@ def test_mm_tiles_exact_with_flags(W, mc, turn, n, bm, whole, halves, k):
         want = ref if bt is None else ref + bt.double()
         assert torch.equal(out, want.to(t)), t
         assert flags.tolist() == [epoch] * segs and cnt.tolist() == [0] * segs
+
+
+@pytest.mark.parametrize("sa,sb", [(254, 0), (0, 254), (254, 60), (104, 1), (20, 100), (0, 0),
+                                   (253, 127), (254, 254)])
+@pytest.mark.parametrize("m", [16, 40, 130])
+def test_mm_extreme_scales(m, sa, sb):
+    """One product an output, of the largest and smallest powers of two: exact where
+    fp32 holds it, its subnormals too, infinite or rounded to nearest past that."""
+    k, n = 64, 64
+    ops = []
+    for rows, s, seed in ((m, sa, 1), (n, sb, 2)):
+        codes = np.zeros((rows, k), np.uint8)
+        codes[:, 35] = np.random.default_rng(seed).integers(0, 16, rows)
+        scales = np.full((rows, 2), s, np.uint8)
+        ops.append((*(torch.from_numpy(v).cuda() for v in ox.pack(codes, scales)),
+                    ox.values(codes, scales, k)))
+    (a, sc_a, av), (b, sc_b, bv) = ops
+    flags, cnt = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    kw = dict(ready_flags=flags, flag_counters=cnt, epoch=1) if m > 64 else {}  # (flags: tiles)
+    out = mc2.mc2_mx4_ag_mm_local(a, sc_a, b, sc_b, k, 1, 0, out_dtype=torch.float32, **kw)
+    assert torch.equal(out.cpu(), torch.from_numpy(av @ bv.T).float())
