@@ -21,10 +21,11 @@
 // which load nothing, and are dropped: rows of a product do not mix, so neither
 // do their NaN.
 //
-// Measured, fc1 and fc2: one token of the layer above 14.8 + 9.6 us (75 MB, 3.1
-// TB/s); 64 tokens, all 128 experts in MX4, 52 + 46 us (316 MB). Bound by chains
+// Measured, fc1 and fc2: one token of the layer above 14.6 + 10.9 us (75 MB, 2.9
+// TB/s); 64 tokens, all 128 experts in MX4, 52 + 52 us (316 MB). Bound by chains
 // of latencies (ids, rows, products, LDS, y, counter, sum) with two workgroups a
-// CU: without any read of w1 the 64 tokens still took 87 of 109 us.
+// CU: without any read of w1 the 64 tokens still take 90 of 112 us, without one of
+// w2 105, without both 80.
 #include "mc2_mx4.hpp"
 #include "mc2_tiles.hpp"
 
@@ -841,9 +842,9 @@ static bool tok_workspace(int64_t T, int K, int64_t H, int64_t I, TokWorkspace& 
 }
 
 // Strips a workgroup: two where twelve workgroups a CU would each have one (us at
-// 1 / 2 / 3 / as many as leave six workgroups a CU: 64 tokens above, MX4, 115 / 108
-// / 116 / 108; 256 tokens of 1024 / 256, 8 of 1024 experts, MX4 209 / 165 / 168 /
-// 271, of 512 experts, bf16 254 / 223 / 228 / 239): the second strip's weights are
+// 1 / 2 / 3 / as many as leave six workgroups a CU: 64 tokens above, MX4, 122 / 111
+// / 119 / 112; 256 tokens of 1024 / 256, 8 of 1024 experts, MX4 219 / 181 / 188 /
+// 315, of 512 experts, bf16 274 / 251 / 280 / 262): the second strip's weights are
 // on their way while the first one's sums are made.
 static int strips_per(int64_t strips, int64_t rows, int64_t cus) {
   return strips * rows >= 12 * cus ? kTokMaxPer : 1;
@@ -861,9 +862,14 @@ static void launch_both(TokArgs a, int rows1, int rows2, int64_t cus, hipStream_
   hipLaunchKernelGGL((tokens_fc2_kernel<W2, MANY>), grid2, dim3(W2::NW * 64), 0, s, a);
 }
 
-// Wide strips from a quarter of the CUs on (us, wide against narrow: 96 wide
-// workgroups of fc1, one token above, 27.0 / 29.5; 32 of them, 37 tokens of 1416 /
-// 200 with 8 experts, 24.4 / 21.6).
+// Wide strips where 64-column ones make workgroups for a quarter of the CUs. fc1, us
+// wide / narrow for bf16 and for MX4 (whose wide strips are of 32 columns), by that
+// number: 96 (one token above) 28.9 / 30.4, 19.3 / 19.1; 72 (six experts) 25.0 / 25.3,
+// 17.9 / 17.7; 64 (40 tokens of 1024 / 512, 8 experts) 23.5 / 23.8, 21.5 / 19.9; 48 (one
+// token, I = 384) 24.5 / 22.9, 17.7 / 16.4; 32 (37 tokens of 1416 / 200, 8 experts)
+// 25.2 / 23.2, 18.8 / 17.3. fc2: 256 (one token, I = 256) 22.4 / 25.1, 15.9 / 19.2; 184
+// (the 37 tokens) 23.2 / 27.2, 17.3 / 21.4; 128 (two experts of 4096 / 1536) 35.5 /
+// 37.5, 19.4 / 18.7; 64 (two of 2048 / 768) 20.2 / 19.9, 13.8 / 12.6.
 template <bool MANY>
 static void launch_tokens(const TokArgs& a, bool mx4, hipStream_t s) {
   const int slots = a.TK < a.El ? a.TK : a.El;

@@ -175,7 +175,7 @@ __global__ __launch_bounds__(TS::NT, TS::BM == 256 ? 1 : 2) void mx4_tile_kernel
 // blocks 4 j + g, g = lane >> 4: a load is 64 contiguous bytes of 16 rows. The 16
 // scale bytes of a row's chunk are one load, from which a lane picks its own.
 // The weights are read once, straight into registers. Bound by latency: 1 x 8192
-// x 3584 (15.6 MB) 5.1 us, 64 x 8192 x 3584 11.6 us.
+// x 3584 (15.6 MB) 5.8 us, 64 x 8192 x 3584 11.6 us.
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ i32x8_t mx4_op(u32x4_t v) {

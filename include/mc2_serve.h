@@ -115,7 +115,10 @@ int mc2_mx4_ag_mm_local(const void* x_gathered, const void* x_scale, const void*
  * sum of the ranks' outs. An id outside [0, num_experts) is skipped and sets
  * MC2_DEVERR_EXPERT_ID. An id may appear more than once in a token. Products
  * accumulate in fp32; h, y and the sum over k are fp32, one rounding to bf16.
- * Every expert named by a slot is read once (per 32 slots of it).
+ * Every expert named by a slot is read once per 32 slots of it, per 16 where
+ * T <= 16. Up to some 64 slots an expert the layer takes less time than those
+ * four calls, beyond that they do (8 experts of 2048 x 1536 and 768 x 2048 in
+ * bf16, K = 8: 64 tokens 64 against 98 us, 128 tokens 118 against 98).
  *
  *   x, out (T, H) bf16; sel (T*K) int32; probs (T*K) fp32.
  *   w_dtype MC2_BF16: w1 (E_l, H, 2I) (gate columns [0, I), up [I, 2I)) and w2
