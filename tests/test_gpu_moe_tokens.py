@@ -395,3 +395,36 @@ def test_two_strips_a_workgroup(mx4, T, H, I, E):
         big.append(b)
     out = own(x, place[sel.long()].to(torch.int32), probs, *big, mx4, ep_rank=0, num_experts=E)
     assert torch.equal(out.cpu(), torch.from_numpy(ref).to(BF))
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("T", [1, 24])
+def test_weights_beyond_2_31_elements_by_the_formula(T, mx4):
+    """64 experts, 2.4e9 elements of w1, of which the first and the last hold numbers
+    and are named: against the formula in 64 bits."""
+    H, I, E = 4096, 4608, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    named = (0, E - 1)
+    w1 = torch.full((E, H, 2 * I), float("nan"), dtype=BF, device="cuda")
+    w2 = torch.full((E, I, H), float("nan"), dtype=BF, device="cuda")
+    for e in named:
+        w1[e] = 0.02 * torch.randn((H, 2 * I), generator=g, device="cuda")
+        w2[e] = 0.02 * torch.randn((I, H), generator=g, device="cuda")
+    x = torch.randn((T, H), generator=g, device="cuda").to(BF)
+    probs = torch.rand((T, 4), generator=g, device="cuda")
+    sel = torch.tensor([0, E - 1, 0, E - 1], dtype=torch.int32, device="cuda").expand(T, 4).contiguous()
+    kw = dict(num_experts=E, ep_rank=0)
+    vals = [(w1[e].double(), w2[e].double()) for e in named]
+    if mx4:
+        (w1, s1), (w2, s2) = (mc2.mc2_mx4_quantize(w, trans=True) for w in (w1, w2))
+        kw.update(w1_scale=s1, w2_scale=s2)
+        vals = [tuple(mc2.mc2_mx4_dequantize(w[e], s[e], k, trans=True, out_dtype=torch.float32).double()
+                      for w, s, k in ((w1, s1, H), (w2, s2, I))) for e in named]
+    out = mc2.mc2_moe_tokens(x, sel, probs, w1, w2, **kw)
+    ref = torch.zeros((T, H), dtype=torch.float64, device="cuda")
+    for i, (v1, v2) in enumerate(vals):
+        a = x.double() @ v1
+        y = (torch.nn.functional.silu(a[:, :I]) * a[:, I:]) @ v2
+        ref += probs[:, i::2].double().sum(1, keepdim=True) * y
+    assert ref.abs().max() > 0.01
+    close(out, ref.cpu())
